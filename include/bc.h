@@ -327,6 +327,184 @@ BC_API size_t bc_workspace_size_argmax(int64_t M, int64_t N, int64_t K, bc_mode 
                                        bc_dtype x_dtype);
 
 /*
+ * bc_add_rmsnorm -- residual addition and root-mean-square norm of M rows:
+ * the step between one projection's fp32 output and the next one's x.
+ *   h = x + residual;  residual <- h (rounded to its type);
+ *   out = h * rsqrt(mean(h^2) + eps) * weight, rounded once (the norm is
+ *   taken of h before the residual's rounding; arithmetic in fp32)
+ *   x         [M][D] x_dtype, device (BC_F32, BC_F16 or BC_BF16, as are the others)
+ *   residual  [M][D] res_dtype, device, read and written; NULL: h = x
+ *   weight    [D] w_dtype, device; NULL: ones
+ *   out       [M][D] out_dtype, device, written; may be x itself when the
+ *             types agree.  What is written may overlap nothing else.
+ *   eps       above 0
+ * Any M up to 2^24 and D up to 2^24.  Pointers need the alignment of their
+ * element type; rows are read in 16-byte pieces when every pointer is 16-byte
+ * aligned and D is a multiple of 8.
+ */
+BC_API bc_status bc_add_rmsnorm(const void *x, bc_dtype x_dtype, void *residual,
+                                bc_dtype res_dtype, const void *weight, bc_dtype w_dtype,
+                                int64_t M, int64_t D, float eps, void *out,
+                                bc_dtype out_dtype, bc_stream_t stream);
+
+/*
+ * bc_add_rmsnorm_q8 -- bc_add_rmsnorm with the output in 8 bits: the layout
+ * of bc_pack_codes at bits = 8 (uint8 codes [M][D], fp16 scale and zero per 64
+ * columns), which bc_matmul_q (BC_MODE_PACKED, bits = 8) reads as its W.
+ *   v = the norm's output in fp32; lo = min(0, min v), hi = max(0, max v) of
+ *   the 64 columns; scale = fp16((hi - lo) / 255), at least 2^-24 and at most
+ *   65504; zero = round(-lo / scale); code = clamp(round(v / scale) + zero, 0, 255)
+ * The range holds 0, so zero is a whole number in 0..255.  fp32 quotients.
+ *   D              a multiple of 64
+ *   codes          uint8 [M][D], device, 8-byte aligned, written
+ *   scales, zeros  fp16 [M][D/64], device, written
+ * x, residual and weight must be 16-byte aligned.
+ */
+BC_API bc_status bc_add_rmsnorm_q8(const void *x, bc_dtype x_dtype, void *residual,
+                                   bc_dtype res_dtype, const void *weight, bc_dtype w_dtype,
+                                   int64_t M, int64_t D, float eps, uint8_t *codes,
+                                   void *scales, void *zeros, bc_stream_t stream);
+
+/*
+ * One projection of a bc_lora_add_batched call.  All pointers are device
+ * pointers.
+ */
+typedef struct bc_lora_desc {
+    const void *x;            /* [M][K], what the projection reads (16-byte aligned) */
+    const void *A;            /* [n_adapters][R][K] (16-byte aligned) */
+    const void *B;            /* [n_adapters][N][R] (16-byte aligned) */
+    float *y;                 /* fp32 [M][N], the projection's output; added to */
+    int64_t N;
+    int64_t K;                /* a multiple of 64 */
+} bc_lora_desc;
+
+/*
+ * bc_lora_add_batched -- low-rank adapters of many requests at once, added to
+ * the outputs of shared projections (bc_matmul_q's y) in one launch per 32
+ * projections: for the rows m of segment i, a = seg_adapter[i],
+ *   y[m] += scaling[a] * B[a] (A[a] x[m])
+ * over the first ranks[a] ranks of R.  Rows of no segment, and rows whose
+ * adapter is none, stay as they are.
+ *   descs        HOST array of `count` descriptors (read before return); no y
+ *                may overlap another y, an x, or the adapters
+ *   R            ranks stored per adapter: a multiple of 8, at most 128
+ *   x_dtype      BC_F32 or BC_BF16;  w_dtype  BC_F16 or BC_BF16 (A and B)
+ *   seg_start    int32 [n_segments + 1], device, not decreasing: segment i is
+ *                the rows seg_start[i] .. seg_start[i + 1] - 1 (empty ones
+ *                are fine; places outside 0..M are cut to it).  One decode
+ *                step: 0, 1, 2, ..., M.  At most 4096 segments.
+ *   seg_adapter  int32 [n_segments], device; outside 0..n_adapters - 1: none
+ *   ranks        int32 [n_adapters], device, or NULL (all R); 0: nothing is
+ *                added.  Ranks behind ranks[a] are not used, whatever they hold.
+ *   scaling      fp32 [n_adapters], device, or NULL (1)
+ * fp32 arithmetic throughout; the order of the sums is fixed, so equal calls
+ * give equal bits.  No workspace.
+ */
+BC_API bc_status bc_lora_add_batched(const bc_lora_desc *descs, int count, int64_t M,
+                                     int64_t R, int64_t n_adapters, bc_dtype x_dtype,
+                                     bc_dtype w_dtype, const int32_t *seg_start,
+                                     const int32_t *seg_adapter, int64_t n_segments,
+                                     const int32_t *ranks, const float *scaling,
+                                     bc_stream_t stream);
+
+/* bc_lora_add -- bc_lora_add_batched for one projection. */
+BC_API bc_status bc_lora_add(const void *x, bc_dtype x_dtype, const void *A, const void *B,
+                             bc_dtype w_dtype, int64_t M, int64_t N, int64_t K, int64_t R,
+                             int64_t n_adapters, const int32_t *seg_start,
+                             const int32_t *seg_adapter, int64_t n_segments,
+                             const int32_t *ranks, const float *scaling, float *y,
+                             bc_stream_t stream);
+
+/*
+ * bc_beam_select -- one step of beam search: over the beams and the
+ * vocabulary of each request, the n_out largest
+ *   total[w][v] = scores[w] + logits[w][v] - log(sum_u exp(logits[w][u]))
+ * in descending order, equal totals by the lowest w * V + v.
+ *   logits        fp32 [batch * beams][V], device (the LM head's y)
+ *   scores        fp32 [batch][beams], device: log-probabilities so far; -inf:
+ *                 the beam is not in use (a search's first step has one beam)
+ *   finished      uint8 [batch][beams], device, or NULL: a finished beam goes
+ *                 on through one candidate, token `pad` at its present score
+ *   eos           a candidate of this token ends its beam (-1: none)
+ *   n_out         candidates per request, at most 64 and at most beams * V
+ *   out_scores    fp32 [batch][n_out], device, written: the totals
+ *   parent        int32 [batch][n_out], device, written: the beam w
+ *   token         int32 [batch][n_out], device, written: v
+ *   out_finished  uint8 [batch][n_out], device, written, or NULL: the parent
+ *                 was finished, or token == eos
+ *   workspace     at least bc_workspace_size_beam() bytes, 256-byte aligned;
+ *                 overlapping calls must not share it
+ * Masked tokens have the logit -inf (NaN counts as -inf, +inf as the largest
+ * finite value); candidates of total -inf fill up the list where no others
+ * are left.  beams <= 32, batch * beams <= 65535, V < 2^30, beams * V < 2^32.
+ * Totals are formed and compared in fp64; the sums of exponentials carry
+ * fp32 exponentials (about 1e-7 relative).
+ */
+BC_API bc_status bc_beam_select(const float *logits, const float *scores,
+                                const uint8_t *finished, int64_t batch, int64_t beams,
+                                int64_t V, int64_t n_out, int32_t eos, int32_t pad,
+                                float *out_scores, int32_t *parent, int32_t *token,
+                                uint8_t *out_finished, void *workspace,
+                                size_t workspace_bytes, bc_stream_t stream);
+
+/* Workspace bytes bc_beam_select needs (0 if the sizes would be rejected). */
+BC_API size_t bc_workspace_size_beam(int64_t batch, int64_t beams, int64_t V, int64_t n_out);
+
+/*
+ * bc_matmul_q_beam -- the LM head's matmul and the beam selection over its
+ * logits (bc_matmul_q_argmax's counterpart for beam search): x holds
+ * batch * beams rows.  Arguments mean what they mean for bc_matmul_q and
+ * bc_beam_select (V = N); workspace of bc_workspace_size_matmul_beam() bytes.
+ */
+BC_API bc_status bc_matmul_q_beam(const void *x, bc_dtype x_dtype, const void *W_or_packed,
+                                  const void *scales, const void *zeros, int64_t batch,
+                                  int64_t beams, int64_t N, int64_t K, int bits,
+                                  int64_t group, bc_mode mode, const float *beam_scores,
+                                  const uint8_t *finished, int64_t n_out, int32_t eos,
+                                  int32_t pad, float *out_scores, int32_t *parent,
+                                  int32_t *token, uint8_t *out_finished, void *workspace,
+                                  size_t workspace_bytes, bc_stream_t stream);
+
+/* Workspace bytes bc_matmul_q_beam needs (0 if the sizes would be rejected). */
+BC_API size_t bc_workspace_size_matmul_beam(int64_t batch, int64_t beams, int64_t N,
+                                            int64_t K, int64_t n_out, bc_mode mode,
+                                            bc_dtype x_dtype);
+
+/*
+ * One state of bc_beam_reorder: beam w of request i is `rows` runs of
+ * row_bytes bytes, run r at data + (i * beams + w) * beam_stride + r * row_stride.
+ * A cache [batch * beams][heads][room][width] with `len` places in use has
+ * rows = heads, row_bytes = len * width bytes, row_stride = room * width bytes.
+ * Runs of different beams may not overlap: either every run of a beam lies
+ * before the next beam, or run r of every beam before run r + 1 of the first
+ * ([layers][batch * beams][...]).
+ */
+typedef struct bc_beam_state {
+    void *data;               /* device, any alignment (16 bytes is fastest) */
+    int64_t rows;
+    int64_t row_bytes;
+    int64_t row_stride;
+    int64_t beam_stride;
+} bc_beam_state;
+
+/*
+ * bc_beam_reorder -- move the beams' states to their new places, in place:
+ *   new[i][w] = old[i][parent[i][w]]
+ * for every state, in one launch per 64 states.  Bytes outside the runs, and
+ * beams that are their own parent, are not touched; a beam whose parent is
+ * outside 0..beams - 1 stays as it is.
+ *   states   HOST array of `count` states (read before return); they may not
+ *            overlap one another or `parent`
+ *   parent   int32, device: parent[i * parent_stride + w] (parent_stride >= beams)
+ * beams <= 32, batch <= 65535; rows * row_bytes of one state below 2^31 of
+ * the widest pieces (16, 8, 4, 2 or 1 bytes) that its address, lengths and
+ * strides are multiples of.
+ */
+BC_API bc_status bc_beam_reorder(const bc_beam_state *states, int count,
+                                 const int32_t *parent, int64_t parent_stride,
+                                 int64_t batch, int64_t beams, bc_stream_t stream);
+
+/*
  * bc_device_timeouts -- number of bounded in-kernel waits (tensor-core
  * pipeline barriers) that ran out on the current device since the library
  * was loaded.  A kernel whose wait runs out stops early, frees its tensor

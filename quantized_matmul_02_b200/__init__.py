@@ -8,6 +8,10 @@ this package on a machine without the built library raises.
 Functions (same names as the C entry points, without the ``bc_`` prefix):
     group_params, quantize_codes, pack_int4, matmul_q, matmul_q_batched,
     workspace_size, workspace_size_batched
+and, around the projections:
+    add_rmsnorm, add_rmsnorm_q8   residual addition and norm before a projection
+    lora_add, lora_add_batched    adapters of many requests beside it
+    beam_select, matmul_q_beam, beam_reorder   beam search after the LM head
 """
 from __future__ import annotations
 
@@ -35,6 +39,9 @@ EXPORTS = ("bc_group_params", "bc_group_minmax", "bc_quantize_codes", "bc_pack_i
            "bc_matmul_q_batched_ex",
            "bc_workspace_size_batched", "bc_matmul_q_noalloc",
            "bc_matmul_q_argmax", "bc_workspace_size_argmax",
+           "bc_add_rmsnorm", "bc_add_rmsnorm_q8", "bc_lora_add", "bc_lora_add_batched",
+           "bc_beam_select", "bc_workspace_size_beam", "bc_matmul_q_beam",
+           "bc_workspace_size_matmul_beam", "bc_beam_reorder",
            "bc_device_timeouts", "bc_set_wait_limit",
            "bc_status_string", "bc_version")
 
@@ -50,6 +57,17 @@ class MatmulDesc(ctypes.Structure):
                 ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
                 ("y", ctypes.c_void_p), ("N", ctypes.c_int64),
                 ("K", ctypes.c_int64)]
+
+
+class LoraDesc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class BeamState(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("row_bytes", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("beam_stride", ctypes.c_int64)]
 
 
 def _load() -> ctypes.CDLL:
@@ -85,6 +103,24 @@ def _load() -> ctypes.CDLL:
     lib.bc_matmul_q_argmax.restype = i32
     lib.bc_workspace_size_argmax.argtypes = [i64, i64, i64, i32, i32]
     lib.bc_workspace_size_argmax.restype = sz
+    f32 = ctypes.c_float
+    lib.bc_add_rmsnorm.argtypes = [P, i32, P, i32, P, i32, i64, i64, f32, P, i32, P]
+    lib.bc_add_rmsnorm_q8.argtypes = [P, i32, P, i32, P, i32, i64, i64, f32, P, P, P, P]
+    lib.bc_lora_add.argtypes = [P, i32, P, P, i32, i64, i64, i64, i64, i64, P, P, i64, P, P,
+                                P, P]
+    lib.bc_lora_add_batched.argtypes = [ctypes.POINTER(LoraDesc), i32, i64, i64, i64, i32, i32,
+                                        P, P, i64, P, P, P]
+    lib.bc_beam_select.argtypes = [P, P, P, i64, i64, i64, i64, i32, i32, P, P, P, P, P, sz, P]
+    lib.bc_workspace_size_beam.argtypes = [i64, i64, i64, i64]
+    lib.bc_workspace_size_beam.restype = sz
+    lib.bc_matmul_q_beam.argtypes = [P, i32, P, P, P, i64, i64, i64, i64, i32, i64, i32, P, P,
+                                     i64, i32, i32, P, P, P, P, P, sz, P]
+    lib.bc_workspace_size_matmul_beam.argtypes = [i64, i64, i64, i64, i64, i32, i32]
+    lib.bc_workspace_size_matmul_beam.restype = sz
+    lib.bc_beam_reorder.argtypes = [ctypes.POINTER(BeamState), i32, P, i64, i64, i64, P]
+    for name in ("bc_add_rmsnorm", "bc_add_rmsnorm_q8", "bc_lora_add", "bc_lora_add_batched",
+                 "bc_beam_select", "bc_matmul_q_beam", "bc_beam_reorder"):
+        getattr(lib, name).restype = i32
     lib.bc_set_wait_limit.argtypes = [ctypes.c_uint64]
     lib.bc_set_wait_limit.restype = i32
     lib.bc_device_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -306,3 +342,353 @@ def matmul_q_argmax(x: torch.Tensor, W: torch.Tensor, scales: Optional[torch.Ten
                                   workspace.numel() * workspace.element_size(),
                                   _stream(stream)), "bc_matmul_q_argmax")
     return token
+
+
+# ---------------------------------------------------------------------------
+# Around the projections: norm, adapters, beam search.  These calls take
+# tensors of one device, run there (also when it is not the current one), and
+# check shapes and types before the C call sees pointers.
+# ---------------------------------------------------------------------------
+def _one_device(what: str, *tensors: Optional[torch.Tensor]) -> torch.device:
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{what}: expected CUDA tensors")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: expected contiguous tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{what}: all tensors must be on one device")
+    return dev
+
+
+def _want(what: str, name: str, t: Optional[torch.Tensor], shape, *dtypes) -> None:
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype not in dtypes):
+        raise ValueError(f"{what}: {name} must be {' or '.join(map(str, dtypes))} {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+
+
+class _Launch:
+    """The device and stream of one call: `with` makes both current, so that
+    outputs and scratch made inside belong to that stream."""
+    __slots__ = ("dev", "stream", "prev_dev", "ctx")
+
+    def __init__(self, what: str, dev: torch.device, stream: Optional[torch.cuda.Stream]):
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"{what}: the stream belongs to another device than the tensors")
+        self.dev, self.stream, self.ctx = dev, stream, None
+
+    def __enter__(self) -> int:
+        if self.stream is not None:
+            self.ctx = torch.cuda.stream(self.stream)
+        elif self.dev.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.dev)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _p(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
+
+
+def _norm_args(what, x, weight, eps, residual):
+    if x.dim() < 1 or x.dtype not in _FLOATS or x.numel() == 0:
+        raise ValueError(f"{what}: x must be a float tensor [..., D] with elements")
+    D = x.shape[-1]
+    if weight is not None:
+        _want(what, "weight", weight, (D,), *_FLOATS)
+    if residual is not None:
+        _want(what, "residual", residual, x.shape, *_FLOATS)
+    return x.numel() // D, D
+
+
+def add_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-6,
+                residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """h = x + residual; residual <- h; returns h / rms(h) * weight over the
+    last dimension, in `out_dtype` (default: x's).  `residual` is updated in
+    place; `out` may be x."""
+    M, D = _norm_args("add_rmsnorm", x, weight, eps, residual)
+    if out is not None:
+        out_dtype = out.dtype
+        _want("add_rmsnorm", "out", out, x.shape, *_FLOATS)
+    elif out_dtype is None:
+        out_dtype = x.dtype
+    elif out_dtype not in _FLOATS:
+        raise ValueError("add_rmsnorm: out_dtype must be float32, float16 or bfloat16")
+    with _Launch("add_rmsnorm", _one_device("add_rmsnorm", x, weight, residual, out), stream) as s:
+        if out is None:
+            out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+        _check(lib.bc_add_rmsnorm(x.data_ptr(), _DT[x.dtype], _p(residual),
+                                  _DT[residual.dtype] if residual is not None else BC_F32,
+                                  _p(weight), _DT[weight.dtype] if weight is not None else BC_F32,
+                                  M, D, eps, out.data_ptr(), _DT[out_dtype], s), "bc_add_rmsnorm")
+    return out
+
+
+def add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-6,
+                   residual: Optional[torch.Tensor] = None,
+                   codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                   zeros: Optional[torch.Tensor] = None, stream=None):
+    """add_rmsnorm with the output as (codes uint8 [..., D], scales, zeros fp16
+    [..., D/64]): what matmul_q reads as packed weights of 8 bits."""
+    what = "add_rmsnorm_q8"
+    M, D = _norm_args(what, x, weight, eps, residual)
+    if D % 64:
+        raise ValueError(f"{what}: D must be a multiple of 64")
+    gs = (*x.shape[:-1], D // 64)
+    if codes is not None:
+        _want(what, "codes", codes, x.shape, torch.uint8)
+    if scales is not None:
+        _want(what, "scales", scales, gs, torch.float16)
+    if zeros is not None:
+        _want(what, "zeros", zeros, gs, torch.float16)
+    with _Launch(what, _one_device(what, x, weight, residual, codes, scales, zeros), stream) as s:
+        if codes is None:
+            codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty(gs, dtype=torch.float16, device=x.device)
+        if zeros is None:
+            zeros = torch.empty(gs, dtype=torch.float16, device=x.device)
+        _check(lib.bc_add_rmsnorm_q8(x.data_ptr(), _DT[x.dtype], _p(residual),
+                                     _DT[residual.dtype] if residual is not None else BC_F32,
+                                     _p(weight), _DT[weight.dtype] if weight is not None else BC_F32,
+                                     M, D, eps, codes.data_ptr(), scales.data_ptr(),
+                                     zeros.data_ptr(), s), "bc_add_rmsnorm_q8")
+    return codes, scales, zeros
+
+
+class LoraDescs:
+    """The projections of one lora_add_batched call (from make_lora_descs);
+    holds its tensors.  Keep it for the steps that use the same buffers."""
+    __slots__ = ("array", "M", "R", "n_adapters", "x_dtype", "w_dtype", "device", "tensors")
+
+
+def make_lora_descs(items: Sequence[tuple]) -> LoraDescs:
+    """items: (x, A, B, y) per projection: x [M][K] fp32 or bf16, A
+    [n_adapters][R][K] and B [n_adapters][N][R] fp16 or bf16, y fp32 [M][N]."""
+    what = "make_lora_descs"
+    if not items:
+        raise ValueError(f"{what}: no projections")
+    x0, A0 = items[0][0], items[0][1]
+    if x0.dim() != 2 or A0.dim() != 3:
+        raise ValueError(f"{what}: x must be [M][K] and A [n_adapters][R][K]")
+    if x0.dtype not in (torch.float32, torch.bfloat16) or A0.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{what}: x must be float32 or bfloat16, adapters float16 or bfloat16")
+    d = LoraDescs()
+    d.M, (d.n_adapters, d.R) = x0.shape[0], A0.shape[:2]
+    d.x_dtype, d.w_dtype, d.tensors = _DT[x0.dtype], _DT[A0.dtype], list(items)
+    d.array = (LoraDesc * len(items))()
+    d.device = _one_device(what, *(t for item in items for t in item))
+    for i, (x, A, B, y) in enumerate(items):
+        if x.dim() != 2 or y.dim() != 2:
+            raise ValueError(f"{what}: x must be [M][K] and y [M][N]")
+        K, N = x.shape[1], y.shape[1]
+        _want(what, "x", x, (d.M, K), x0.dtype)
+        _want(what, "A", A, (d.n_adapters, d.R, K), A0.dtype)
+        _want(what, "B", B, (d.n_adapters, N, d.R), A0.dtype)
+        _want(what, "y", y, (d.M, N), torch.float32)
+        d.array[i] = LoraDesc(x.data_ptr(), A.data_ptr(), B.data_ptr(), y.data_ptr(), N, K)
+    return d
+
+
+def lora_add_batched(descs: LoraDescs, seg_start: torch.Tensor, seg_adapter: torch.Tensor,
+                     ranks: Optional[torch.Tensor] = None,
+                     scaling: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y[m] += scaling[a] * B[a] (A[a] x[m]) for every projection of `descs`:
+    the rows seg_start[i] .. seg_start[i+1]-1 use adapter a = seg_adapter[i]
+    (outside 0..n_adapters-1: none).  seg_start int32 [S+1], seg_adapter int32
+    [S]; ranks int32 and scaling fp32 [n_adapters], or None."""
+    what = "lora_add_batched"
+    S = seg_adapter.numel()
+    _want(what, "seg_adapter", seg_adapter, (S,), torch.int32)
+    _want(what, "seg_start", seg_start, (S + 1,), torch.int32)
+    if ranks is not None:
+        _want(what, "ranks", ranks, (descs.n_adapters,), torch.int32)
+    if scaling is not None:
+        _want(what, "scaling", scaling, (descs.n_adapters,), torch.float32)
+    dev = _one_device(what, seg_start, seg_adapter, ranks, scaling)
+    if dev != descs.device:
+        raise ValueError(f"{what}: all tensors must be on one device")
+    with _Launch(what, dev, stream) as s:
+        _check(lib.bc_lora_add_batched(descs.array, len(descs.array), descs.M, descs.R,
+                                       descs.n_adapters, descs.x_dtype, descs.w_dtype,
+                                       seg_start.data_ptr(), seg_adapter.data_ptr(), S,
+                                       _p(ranks), _p(scaling), s), "bc_lora_add_batched")
+
+
+def lora_add(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, y: torch.Tensor,
+             seg_start: torch.Tensor, seg_adapter: torch.Tensor,
+             ranks: Optional[torch.Tensor] = None, scaling: Optional[torch.Tensor] = None,
+             stream=None) -> torch.Tensor:
+    """lora_add_batched for one projection; returns y."""
+    lora_add_batched(make_lora_descs([(x, A, B, y)]), seg_start, seg_adapter, ranks, scaling, stream)
+    return y
+
+
+def workspace_size_beam(batch: int, beams: int, V: int, n_out: int) -> int:
+    return int(lib.bc_workspace_size_beam(batch, beams, V, n_out))
+
+
+def _beam_out(what, dev, batch, n_out, out):
+    if out is None:
+        return (torch.empty((batch, n_out), dtype=torch.float32, device=dev),
+                torch.empty((batch, n_out), dtype=torch.int32, device=dev),
+                torch.empty((batch, n_out), dtype=torch.int32, device=dev),
+                torch.empty((batch, n_out), dtype=torch.uint8, device=dev))
+    for t, name, dt in zip(out, ("out scores", "parent", "token", "out finished"),
+                           (torch.float32, torch.int32, torch.int32, torch.uint8)):
+        _want(what, name, t, (batch, n_out), dt)
+    return tuple(out)
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int,
+                finished: Optional[torch.Tensor] = None, eos: int = -1, pad: int = 0,
+                out: Optional[Sequence[torch.Tensor]] = None,
+                workspace: Optional[torch.Tensor] = None, stream=None):
+    """The n_out best continuations of each request: logits fp32
+    [batch * beams][V], scores fp32 [batch][beams], finished uint8 (or bool)
+    [batch][beams].  Returns (scores fp32, parent int32, token int32, finished
+    uint8), each [batch][n_out], in descending order of total."""
+    what = "beam_select"
+    if scores.dim() != 2 or logits.dim() != 2:
+        raise ValueError(f"{what}: logits must be [batch * beams][V], scores [batch][beams]")
+    batch, beams = scores.shape
+    V = logits.shape[1]
+    _want(what, "logits", logits, (batch * beams, V), torch.float32)
+    _want(what, "scores", scores, (batch, beams), torch.float32)
+    if finished is not None:
+        _want(what, "finished", finished, (batch, beams), torch.uint8, torch.bool)
+    dev = _one_device(what, logits, scores, finished, workspace, *(out or ()))
+    with _Launch(what, dev, stream) as s:
+        o = _beam_out(what, dev, batch, n_out, out)
+        need = workspace_size_beam(batch, beams, V, n_out)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(lib.bc_beam_select(logits.data_ptr(), scores.data_ptr(), _p(finished), batch, beams,
+                                  V, n_out, eos, pad, o[0].data_ptr(), o[1].data_ptr(),
+                                  o[2].data_ptr(), o[3].data_ptr(), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), s),
+               "bc_beam_select")
+    return o
+
+
+def workspace_size_matmul_beam(batch: int, beams: int, N: int, K: int, n_out: int, mode: int,
+                               x_dtype: int = BC_F32) -> int:
+    return int(lib.bc_workspace_size_matmul_beam(batch, beams, N, K, n_out, mode, x_dtype))
+
+
+def matmul_q_beam(x: torch.Tensor, W: torch.Tensor, scales: Optional[torch.Tensor],
+                  zeros: Optional[torch.Tensor], bits: int, group: int, mode: int,
+                  beam_scores: torch.Tensor, n_out: int,
+                  finished: Optional[torch.Tensor] = None, eos: int = -1, pad: int = 0,
+                  out: Optional[Sequence[torch.Tensor]] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None):
+    """The LM head's matmul_q on x [batch * beams][K] and beam_select over its
+    logits, in one call; returns what beam_select returns."""
+    what = "matmul_q_beam"
+    if beam_scores.dim() != 2 or x.dim() != 2 or x.shape[0] != beam_scores.numel():
+        raise ValueError(f"{what}: x must be [batch * beams][K], beam_scores [batch][beams]")
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{what}: x must be float32 or bfloat16")
+    batch, beams = beam_scores.shape
+    K, N = x.shape[1], W.shape[0]
+    packed = mode == BC_MODE_PACKED
+    if packed:
+        _want(what, "W", W, (N, K * bits // 8), torch.uint8)
+    else:
+        _want(what, "W", W, (N, K), torch.float16)
+    if packed or bits != 16:
+        groups = K // 64 if group == 64 else 1
+        sz = torch.float16 if packed else torch.int32 if mode == BC_MODE_RUNTIME_RANGE else torch.float32
+        _want(what, "scales", scales, (N, groups), sz)
+        if mode != BC_MODE_RUNTIME_RANGE:
+            _want(what, "zeros", zeros, (N, groups), sz)
+    _want(what, "beam_scores", beam_scores, (batch, beams), torch.float32)
+    if finished is not None:
+        _want(what, "finished", finished, (batch, beams), torch.uint8, torch.bool)
+    dev = _one_device(what, x, W, scales, zeros, beam_scores, finished, workspace, *(out or ()))
+    with _Launch(what, dev, stream) as s:
+        o = _beam_out(what, dev, batch, n_out, out)
+        need = workspace_size_matmul_beam(batch, beams, N, K, n_out, mode, _DT[x.dtype])
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(lib.bc_matmul_q_beam(x.data_ptr(), _DT[x.dtype], W.data_ptr(), _p(scales), _p(zeros),
+                                    batch, beams, N, K, bits, group, mode, beam_scores.data_ptr(),
+                                    _p(finished), n_out, eos, pad, o[0].data_ptr(), o[1].data_ptr(),
+                                    o[2].data_ptr(), o[3].data_ptr(), workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), s),
+               "bc_matmul_q_beam")
+    return o
+
+
+class BeamStates:
+    """States of beam_reorder (from make_beam_states); holds its tensors."""
+    __slots__ = ("array", "beams_total", "device", "tensors")
+
+
+def make_beam_states(tensors: Sequence[torch.Tensor]) -> BeamStates:
+    """tensors: views [batch * beams, ...] of caches or histories, of any type.
+    Dimension 0 counts the beams; the others have to be runs of contiguous
+    elements at one stride (a cache [batch * beams, heads, room, width] cut to
+    its first `len` places is heads runs of len * width elements)."""
+    what = "make_beam_states"
+    if not tensors:
+        raise ValueError(f"{what}: no states")
+    st = BeamStates()
+    st.beams_total, st.device, st.tensors = tensors[0].shape[0], tensors[0].device, list(tensors)
+    st.array = (BeamState * len(tensors))()
+    for i, t in enumerate(tensors):
+        if not t.is_cuda or t.device != st.device:
+            raise ValueError(f"{what}: all states must be on one CUDA device")
+        shape, strides = t.shape, t.stride()
+        if shape[0] != st.beams_total or t.numel() == 0:
+            raise ValueError(f"{what}: every state must be [batch * beams, ...] with elements")
+        run, rows, row_stride, size = 1, 1, 0, t.element_size()
+        for n, s in zip(reversed(shape[1:]), reversed(strides[1:])):
+            if n == 1:
+                continue
+            if rows == 1 and s == run:
+                run *= n
+            elif rows == 1:
+                rows, row_stride = n, s
+            elif s == row_stride * rows:
+                rows *= n
+            else:
+                raise ValueError(f"{what}: state {i} is not runs of contiguous elements at one stride")
+        if rows > 1 and row_stride < run:
+            raise ValueError(f"{what}: state {i} overlaps itself")
+        beam = strides[0] if shape[0] > 1 else max(strides[0], run)
+        st.array[i] = BeamState(t.data_ptr(), rows, run * size, row_stride * size, beam * size)
+    return st
+
+
+def beam_reorder(states, parent: torch.Tensor, stream=None) -> None:
+    """new[i][w] = old[i][parent[i][w]] in place for every state: `states` are
+    tensors as make_beam_states takes them, or its result; parent int32
+    [batch][beams] (a view of wider rows is fine)."""
+    what = "beam_reorder"
+    if not isinstance(states, BeamStates):
+        states = make_beam_states(states)
+    if parent.dim() != 2 or parent.dtype != torch.int32 or (parent.shape[1] > 1 and parent.stride(1) != 1):
+        raise ValueError(f"{what}: parent must be int32 [batch][beams]")
+    if parent.device != states.device:
+        raise ValueError(f"{what}: all tensors must be on one device")
+    batch, beams = parent.shape
+    if batch * beams != states.beams_total:
+        raise ValueError(f"{what}: the states have {states.beams_total} beams, parent {batch} x {beams}")
+    with _Launch(what, states.device, stream) as s:
+        _check(lib.bc_beam_reorder(states.array, len(states.array), parent.data_ptr(),
+                                   parent.stride(0) if batch > 1 else beams, batch, beams, s),
+               "bc_beam_reorder")

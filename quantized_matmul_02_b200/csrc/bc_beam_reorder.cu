@@ -1,0 +1,151 @@
+// bc_beam_reorder.cu -- move the beams' states (caches, token histories) to
+// their new places after a selection, in place and for many states at once:
+// new[i][w] = old[i][parent[i][w]].
+//
+// A thread owns the same few bytes of all beams of one request: it loads what
+// the moving beams need into registers, then stores.  No byte is read after
+// it may have been overwritten (only its owner writes it), so no second
+// buffer is needed, and beams that stay where they are cost nothing.
+// HBM bound: each moved beam is written once and its parent read once (beams
+// that share a parent find it in L1).
+#include "bc_internal.cuh"
+
+namespace bc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxStates = 64;         // per launch (kernel parameters)
+constexpr int kMaxBeams = 32;
+
+struct State {
+    uint8_t *data;
+    int64_t row_stride, beam_stride;
+    uint32_t rows, units;              // units of `vec` bytes per row
+    int vec;
+};
+struct ReorderArgs {
+    State st[kMaxStates];
+    const int32_t *parent;
+    int64_t parent_stride;
+    int beams;
+};
+
+template <typename T, int WMAX>
+__device__ __forceinline__ void move(const State &st, uint8_t *base, const int *src, uint32_t moved,
+                                     int beams) {
+    const uint32_t total = st.rows * st.units;
+    for (uint32_t e = blockIdx.x * kThreads + threadIdx.x; e < total; e += gridDim.x * kThreads) {
+        const uint32_t row = e / st.units, u = e - row * st.units;
+        uint8_t *p = base + row * st.row_stride + (int64_t)u * sizeof(T);
+        T v[WMAX];
+#pragma unroll
+        for (int w = 0; w < WMAX; ++w)
+            if (moved >> w & 1) v[w] = *reinterpret_cast<const T *>(p + src[w] * st.beam_stride);
+#pragma unroll
+        for (int w = 0; w < WMAX; ++w)
+            if (moved >> w & 1) *reinterpret_cast<T *>(p + w * st.beam_stride) = v[w];
+    }
+}
+
+// grid (chunks, batch, states)
+template <int WMAX>
+__global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant__ ReorderArgs a) {
+    __shared__ int src[kMaxBeams];
+    __shared__ uint32_t moved_sh;
+    if (threadIdx.x < 32) {
+        const int w = threadIdx.x;
+        int p = w;
+        if (w < a.beams) {
+            p = a.parent[blockIdx.y * a.parent_stride + w];
+            if (p < 0 || p >= a.beams) p = w;          // no such beam: stays as it is
+        }
+        src[w] = p;
+        const uint32_t m = __ballot_sync(0xffffffffu, p != w);
+        if (w == 0) moved_sh = m;
+    }
+    __syncthreads();
+    const uint32_t moved = moved_sh;
+    if (!moved) return;
+    const State &st = a.st[blockIdx.z];
+    uint8_t *base = st.data + (int64_t)blockIdx.y * a.beams * st.beam_stride;
+    switch (st.vec) {
+    case 16: move<uint4, WMAX>(st, base, src, moved, a.beams); break;
+    case 8: move<uint2, WMAX>(st, base, src, moved, a.beams); break;
+    case 4: move<uint32_t, WMAX>(st, base, src, moved, a.beams); break;
+    case 2: move<uint16_t, WMAX>(st, base, src, moved, a.beams); break;
+    default: move<uint8_t, WMAX>(st, base, src, moved, a.beams); break;
+    }
+}
+
+// Widest access that the address, the length and the strides of a state allow.
+int vec_of(const bc_beam_state &d) {
+    const uint64_t bits = reinterpret_cast<uintptr_t>(d.data) | (uint64_t)d.row_bytes |
+                          (uint64_t)d.beam_stride | (d.rows > 1 ? (uint64_t)d.row_stride : 0);
+    return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+}
+
+}  // namespace
+}  // namespace bc
+
+using namespace bc;
+
+extern "C" bc_status bc_beam_reorder(const bc_beam_state *states, int count, const int32_t *parent,
+                                     int64_t parent_stride, int64_t batch, int64_t beams,
+                                     bc_stream_t stream) {
+    if (!states || count <= 0 || !parent || batch <= 0 || beams <= 0) return BC_ERR_INVALID_ARG;
+    if (parent_stride < beams) return BC_ERR_INVALID_ARG;
+    if (beams > kMaxBeams || batch > 65535 || parent_stride > (int64_t)1 << 40) return BC_ERR_UNSUPPORTED;
+    if (!aligned(parent, 4)) return BC_ERR_ALIGNMENT;
+    for (int i = 0; i < count; ++i) {
+        const bc_beam_state &d = states[i];
+        if (!d.data || d.rows <= 0 || d.row_bytes <= 0 || d.row_stride < 0 || d.beam_stride < d.row_bytes)
+            return BC_ERR_INVALID_ARG;
+        // rows of different beams must not share bytes: beams outside rows, or rows outside beams
+        const int64_t lim = (int64_t)1 << 46;
+        if (d.rows > lim || d.row_bytes > lim || d.row_stride > lim || d.beam_stride > lim)
+            return BC_ERR_UNSUPPORTED;
+        if (d.rows > 1) {
+            const unsigned __int128 in = (unsigned __int128)(d.rows - 1) * d.row_stride + d.row_bytes;
+            const unsigned __int128 all =
+                (unsigned __int128)(batch * beams - 1) * d.beam_stride + d.row_bytes;
+            const bool beams_outside = d.row_stride >= d.row_bytes && (unsigned __int128)d.beam_stride >= in;
+            const bool rows_outside = (unsigned __int128)d.row_stride >= all;
+            if (!beams_outside && !rows_outside) return BC_ERR_INVALID_ARG;
+        }
+        const int vec = vec_of(d);
+        if ((unsigned __int128)(d.row_bytes / vec) * d.rows >= (1ull << 31)) return BC_ERR_UNSUPPORTED;
+        for (int j = 0; j < i; ++j)
+            if (states[j].data == d.data) return BC_ERR_INVALID_ARG;   // would be moved twice
+        const unsigned __int128 end = (unsigned __int128)reinterpret_cast<uintptr_t>(d.data) +
+            (unsigned __int128)(d.rows - 1) * (d.rows > 1 ? d.row_stride : 0) +
+            (unsigned __int128)(batch * beams - 1) * d.beam_stride + d.row_bytes;
+        const unsigned __int128 p0 = reinterpret_cast<uintptr_t>(parent);
+        const unsigned __int128 p1 = p0 + 4 * ((unsigned __int128)(batch - 1) * parent_stride + beams);
+        if (p0 < end && reinterpret_cast<uintptr_t>(d.data) < p1) return BC_ERR_INVALID_ARG;
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    ReorderArgs a;
+    a.parent = parent;
+    a.parent_stride = parent_stride;
+    a.beams = (int)beams;
+    for (int i = 0; i < count; i += kMaxStates) {
+        const int n = count - i < kMaxStates ? count - i : kMaxStates;
+        uint64_t most = 0;
+        for (int j = 0; j < n; ++j) {
+            const bc_beam_state &d = states[i + j];
+            const int vec = vec_of(d);
+            const uint64_t units = (uint64_t)d.row_bytes / vec;
+            a.st[j] = State{static_cast<uint8_t *>(d.data), d.rows > 1 ? d.row_stride : 0, d.beam_stride,
+                            (uint32_t)d.rows, (uint32_t)units, vec};
+            if (units * d.rows > most) most = units * d.rows;
+        }
+        const dim3 grid((unsigned)((most + kThreads - 1) / kThreads), (unsigned)batch, (unsigned)n);
+        if (beams <= 4) reorder_kernel<4><<<grid, kThreads, 0, s>>>(a);
+        else if (beams <= 8) reorder_kernel<8><<<grid, kThreads, 0, s>>>(a);
+        else if (beams <= 16) reorder_kernel<16><<<grid, kThreads, 0, s>>>(a);
+        else reorder_kernel<32><<<grid, kThreads, 0, s>>>(a);
+        const bc_status st = cuda_status();
+        if (st != BC_OK) return st;
+    }
+    return BC_OK;
+}

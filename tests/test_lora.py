@@ -1,0 +1,191 @@
+"""Low-rank adapters of many requests (bc_lora_add, bc_lora_add_batched)
+against the formula in 64 bits, and the refusals."""
+import math
+
+import pytest
+import torch
+
+FAKE = 0x10000                    # aligned non-null address: never dereferenced
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+def _make(M, K, Ns, R, n, xt, wt, seed, mixed=True):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x = r(M, K).to(xt)
+    mats = [((r(n, R, K) / math.sqrt(K)).to(wt), (r(n, N, R) / math.sqrt(R)).to(wt), r(M, N)) for N in Ns]
+    ranks = torch.randint(0, R + 1, (n,), generator=g, device="cuda", dtype=torch.int32) if mixed else None
+    scaling = 0.2 + torch.rand((n,), generator=g, device="cuda")
+    return x, mats, ranks, scaling
+
+
+def _check(x, A, B, y0, y, start, adapter, ranks, scaling):
+    """Every row against the formula; rows without an adapter unchanged.
+
+    Bound, relative to S = |c| sum_r (sum_k |A x|) |B|: an fp32 x, and v, enter
+    as two tf32 pieces (2^-22 each); a tensor-core step of 8 products is taken
+    as 9 additions of 2^-23.  A warp takes 2 x 4 steps per 32 of the K / 256
+    that one of 8 x 8 warps has at most ceil(K / 2048) times; 15 additions join
+    the warps and blocks, one product brings the scale; ranks take 4 steps per
+    16.  Then y: one addition (2^-24 of the result)."""
+    n, R, K = A.shape
+    steps1, steps2 = 8 * math.ceil(K / 2048), 4 * math.ceil(R / 16)
+    rel = 2 * 2.0 ** -22 + (9 * steps1 + 16 + 9 * steps2) * 2.0 ** -23
+    seen = torch.zeros(x.shape[0], dtype=torch.bool)
+    for i in range(adapter.numel()):
+        a, s0, s1 = int(adapter[i]), int(start[i]), int(start[i + 1])
+        keep = 0 if a < 0 or a >= n else R if ranks is None else int(ranks[a])
+        if keep == 0 or s0 == s1:
+            continue
+        seen[s0:s1] = True
+        c = 1.0 if scaling is None else float(scaling[a])
+        Ad, Bd, xd = A[a, :keep].double(), B[a, :, :keep].double(), x[s0:s1].double()
+        want = y0[s0:s1].double() + c * (xd @ Ad.T) @ Bd.T
+        S = abs(c) * (xd.abs() @ Ad.abs().T) @ Bd.abs().T
+        err = (y[s0:s1].double() - want).abs()
+        bound = rel * S + 2.0 ** -24 * (want.abs() + rel * S)
+        assert bool((err <= bound).all()), (i, a, float((err / bound).max()))
+    assert torch.equal(y[~seen], y0[~seen])
+
+
+def _run(q, x, mats, start, adapter, ranks, scaling):
+    st = torch.tensor(start, dtype=torch.int32, device="cuda")
+    ad = torch.tensor(adapter, dtype=torch.int32, device="cuda")
+    old = [m[2].clone() for m in mats]
+    q.lora_add_batched(q.make_lora_descs([(x, A, B, y) for A, B, y in mats]), st, ad, ranks, scaling)
+    for (A, B, y), y0 in zip(mats, old):
+        _check(x, A, B, y0, y, start, adapter, ranks, scaling)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("xt", [F32, BF16])
+@pytest.mark.parametrize("wt", [F16, BF16])
+@pytest.mark.parametrize("M,K,Ns,R,n", [
+    (1, 64, (1,), 8, 1), (1, 896, (896, 128, 128), 16, 4), (3, 128, (33,), 8, 2), (17, 192, (100, 64), 24, 3),
+    (64, 1024, (260,), 32, 20), (130, 320, (77,), 64, 40), (256, 448, (129,), 128, 7), (256, 64, (32,), 16, 1)])
+def test_decode_one_row_a_request(cuda_lib, M, K, Ns, R, n, xt, wt):
+    x, mats, ranks, scaling = _make(M, K, Ns, R, n, xt, wt, M + K)
+    g = torch.Generator().manual_seed(M)
+    adapter = torch.randint(-1, n + 1, (M,), generator=g).tolist()    # some without one, on both sides
+    if M == 1:
+        adapter = [n - 1]
+        ranks = None
+    _run(cuda_lib, x, mats, list(range(M + 1)), adapter, ranks, scaling)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("xt", [F32, BF16])
+@pytest.mark.parametrize("wt", [F16, BF16])
+@pytest.mark.parametrize("start,K,Ns,R", [
+    ([0, 300], 128, (64,), 16), ([0, 1, 2, 259], 192, (36, 31), 8), ([0, 0, 100, 100, 257, 400], 896, (130,), 32),
+    ([5, 70, 200, 390], 256, (40,), 128), ([0, 64, 128, 192, 256, 320], 64, (256,), 40),
+    ([0, 1000], 2176, (45,), 24), ([0, 3, 17, 33, 66, 130, 259, 516, 1030], 128, (68,), 16)])
+def test_prompts(cuda_lib, start, K, Ns, R, xt, wt):
+    S, M = len(start) - 1, start[-1] + 10                             # rows behind the last segment
+    x, mats, ranks, scaling = _make(M, K, Ns, R, 3, xt, wt, M + K)
+    if ranks is not None:
+        ranks[0] = R
+    _run(cuda_lib, x, mats, start, [i % 4 - (i == 5) for i in range(S)], ranks, scaling)
+
+
+@pytest.mark.gpu
+def test_many_short_segments(cuda_lib):
+    """More rows than are ordered by adapter, in segments of 0 to 5 rows."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 6, (700,), generator=g).tolist()
+    start = [0]
+    for n in lens:
+        start.append(start[-1] + n)
+    x, mats, ranks, scaling = _make(start[-1], 128, (50,), 16, 9, F32, BF16, 4)
+    _run(cuda_lib, x, mats, start, torch.randint(-1, 9, (700,), generator=g).tolist(), ranks, scaling)
+
+
+@pytest.mark.gpu
+def test_no_rows_no_ranks(cuda_lib):
+    """Segments that are all empty, all without an adapter, or of rank 0."""
+    x, mats, _, scaling = _make(40, 64, (24,), 8, 2, F32, F16, 5)
+    y0 = mats[0][2].clone()
+    for start, adapter, ranks in (([0, 0, 0], [0, 1], None), ([0, 20, 40], [-1, 2], None), ([0, 20, 40], [0, 1], [0, -3])):
+        rk = None if ranks is None else torch.tensor(ranks, dtype=torch.int32, device="cuda")
+        _run(cuda_lib, x, mats, start, adapter, rk if rk is None else rk.clamp(min=0), scaling)
+        assert torch.equal(mats[0][2], y0)
+
+
+@pytest.mark.gpu
+def test_unused_ranks_and_rows_are_not_read(cuda_lib):
+    """NaN behind an adapter's rank, in other adapters and in rows of no
+    segment stays out of the results; places outside 0..M are cut."""
+    M, K, N, R = 24, 128, 40, 16
+    for rank in (1, 5, 8, 13):
+        x, mats, _, scaling = _make(M, K, (N,), R, 3, F32, BF16, rank)
+        A, B, y = mats[0]
+        ranks = torch.full((3,), rank, dtype=torch.int32, device="cuda")
+        A[:, rank:] = float("nan")
+        B[:, :, rank:] = float("nan")
+        A[2], B[2] = float("nan"), float("nan")
+        x[20:] = float("nan")
+        _run(cuda_lib, x, mats, [0, 9, 20], [1, 0], ranks, scaling)
+        assert not torch.isnan(y).any()
+    x, mats, ranks, scaling = _make(M, K, (N,), R, 3, F32, F16, 9, mixed=False)
+    y0 = mats[0][2].clone()
+    st = torch.tensor([-5, 10, 1000], dtype=torch.int32, device="cuda")
+    ad = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    cuda_lib.lora_add(x, mats[0][0], mats[0][1], mats[0][2], st, ad, scaling=scaling)
+    _check(x, *mats[0][:2], y0, mats[0][2], [0, 10, M], [1, 0], None, scaling)
+
+
+@pytest.mark.gpu
+def test_same_bits_every_time_and_unaligned_y(cuda_lib):
+    x, mats, ranks, scaling = _make(300, 512, (96,), 32, 4, BF16, BF16, 11)
+    A, B, y = mats[0]
+    start = torch.tensor([0, 100, 101, 300], dtype=torch.int32, device="cuda")
+    adapter = torch.tensor([0, 3, 2], dtype=torch.int32, device="cuda")
+    buf = torch.zeros(300 * 96 + 1, device="cuda")
+    off = buf[1:].view(300, 96)                       # rows that begin off 16 bytes
+    off.copy_(y)
+    y2 = y.clone()
+    for t in (y, y2, off):
+        cuda_lib.lora_add(x, A, B, t, start, adapter, ranks, scaling)
+    assert torch.equal(y, y2) and torch.equal(y, off)
+
+
+@pytest.mark.gpu
+def test_more_projections_than_one_launch(cuda_lib):
+    x, mats, ranks, scaling = _make(5, 64, (16,) * 35, 8, 2, F32, F16, 12)
+    _run(cuda_lib, x, mats, [0, 2, 5], [1, 0], None, None)
+
+
+def test_lora_rejects_on_host():
+    import quantized_matmul_02_b200 as q
+    at = [FAKE + (i << 26) for i in range(8)]
+    ok = dict(x=at[0], xt=0, A=at[1], B=at[2], wt=1, M=4, N=32, K=64, R=8, n=2, start=at[3], adapter=at[4], S=4,
+              ranks=None, scaling=None, y=at[5], stream=None)
+    call = lambda **kw: q.lib.bc_lora_add(*{**ok, **kw}.values())  # noqa: E731
+    for k in ("x", "A", "B", "start", "adapter", "y"):
+        assert call(**{k: None}) == 1
+    for k in ("M", "N", "K", "R", "n", "S"):
+        assert call(**{k: 0}) == 1 and call(**{k: -8}) == 1
+    assert call(K=96) == 1 and call(R=12) == 1 and call(R=136) == 2 and call(S=4097) == 2
+    assert call(xt=1) == 2 and call(wt=0) == 2 and call(M=1 << 25) == 2 and call(N=1 << 30) == 2
+    assert call(x=at[0] + 8) == 3 and call(A=at[1] + 2) == 3 and call(y=at[5] + 2) == 3 and call(start=at[3] + 1) == 3
+    assert call(y=at[0]) == 1 and call(y=at[2] + 64) == 1 and call(y=at[3]) == 1
+    arr = (q.LoraDesc * 2)(*[q.LoraDesc(at[0], at[1], at[2], at[5], 32, 64)] * 2)
+    assert q.lib.bc_lora_add_batched(arr, 2, 4, 8, 2, 0, 1, at[3], at[4], 4, None, None, None) == 1   # one y twice
+    assert q.lib.bc_lora_add_batched(None, 1, 4, 8, 2, 0, 1, at[3], at[4], 4, None, None, None) == 1
+    with pytest.raises(ValueError):
+        q.make_lora_descs([(torch.zeros(2, 64), torch.zeros(1, 8, 64).half(), torch.zeros(1, 4, 8).half(), torch.zeros(2, 4))])
+    with pytest.raises(ValueError):
+        q.make_lora_descs([])
+
+
+@pytest.mark.gpu
+def test_lora_wrapper_refuses(cuda_lib):
+    x, mats, _, scaling = _make(4, 64, (24,), 8, 2, F32, F16, 5)
+    A, B, y = mats[0]
+    st = torch.arange(5, dtype=torch.int32, device="cuda")
+    ad = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for bad in ((x, A, B[:, :20].contiguous(), y, st, ad), (x, A, B, y[:3], st, ad), (x, A, B.float(), y, st, ad),
+                (x, A, B, y, st[:4], ad), (x, A, B, y, st.long(), ad), (x.half(), A, B, y, st, ad),
+                (x, A, B, y.cpu(), st, ad), (x, A.transpose(1, 2), B, y, st, ad)):
+        with pytest.raises(ValueError):
+            cuda_lib.lora_add(*bad)
