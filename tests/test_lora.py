@@ -32,7 +32,7 @@ def _check(x, A, B, y0, y, start, adapter, ranks, scaling):
     steps1, steps2 = 8 * math.ceil(K / 2048), 4 * math.ceil(R / 16)
     rel = 2 * 2.0 ** -22 + (9 * steps1 + 16 + 9 * steps2) * 2.0 ** -23
     seen = torch.zeros(x.shape[0], dtype=torch.bool)
-    for i in range(adapter.numel()):
+    for i in range(len(adapter)):
         a, s0, s1 = int(adapter[i]), int(start[i]), int(start[i + 1])
         keep = 0 if a < 0 or a >= n else R if ranks is None else int(ranks[a])
         if keep == 0 or s0 == s1:
