@@ -380,7 +380,7 @@ typedef struct bc_lora_desc {
 
 /*
  * bc_lora_add_batched -- low-rank adapters of many requests at once, added to
- * the outputs of shared projections (bc_matmul_q's y) in one launch per 32
+ * the outputs of shared projections (bc_matmul_q's y), two launches per 32
  * projections: for the rows m of segment i, a = seg_adapter[i],
  *   y[m] += scaling[a] * B[a] (A[a] x[m])
  * over the first ranks[a] ranks of R.  Rows of no segment, and rows whose
@@ -397,15 +397,24 @@ typedef struct bc_lora_desc {
  *   ranks        int32 [n_adapters], device, or NULL (all R); 0: nothing is
  *                added.  Ranks behind ranks[a] are not used, whatever they hold.
  *   scaling      fp32 [n_adapters], device, or NULL (1)
+ *   workspace    at least bc_workspace_size_lora() bytes, 256-byte aligned;
+ *                its contents on entry do not matter; overlapping calls must
+ *                not share it
  * fp32 arithmetic throughout; the order of the sums is fixed, so equal calls
- * give equal bits.  No workspace.
+ * give equal bits.
  */
 BC_API bc_status bc_lora_add_batched(const bc_lora_desc *descs, int count, int64_t M,
                                      int64_t R, int64_t n_adapters, bc_dtype x_dtype,
                                      bc_dtype w_dtype, const int32_t *seg_start,
                                      const int32_t *seg_adapter, int64_t n_segments,
                                      const int32_t *ranks, const float *scaling,
+                                     void *workspace, size_t workspace_bytes,
                                      bc_stream_t stream);
+
+/* Workspace bytes bc_lora_add_batched needs (reads N and K of each descriptor;
+ * 0 if the sizes would be rejected). */
+BC_API size_t bc_workspace_size_lora(const bc_lora_desc *descs, int count, int64_t M,
+                                     int64_t R, int64_t n_adapters, int64_t n_segments);
 
 /* bc_lora_add -- bc_lora_add_batched for one projection. */
 BC_API bc_status bc_lora_add(const void *x, bc_dtype x_dtype, const void *A, const void *B,
@@ -413,7 +422,7 @@ BC_API bc_status bc_lora_add(const void *x, bc_dtype x_dtype, const void *A, con
                              int64_t n_adapters, const int32_t *seg_start,
                              const int32_t *seg_adapter, int64_t n_segments,
                              const int32_t *ranks, const float *scaling, float *y,
-                             bc_stream_t stream);
+                             void *workspace, size_t workspace_bytes, bc_stream_t stream);
 
 /*
  * bc_beam_select -- one step of beam search: over the beams and the

@@ -40,7 +40,7 @@ EXPORTS = ("bc_group_params", "bc_group_minmax", "bc_quantize_codes", "bc_pack_i
            "bc_workspace_size_batched", "bc_matmul_q_noalloc",
            "bc_matmul_q_argmax", "bc_workspace_size_argmax",
            "bc_add_rmsnorm", "bc_add_rmsnorm_q8", "bc_lora_add", "bc_lora_add_batched",
-           "bc_beam_select", "bc_workspace_size_beam", "bc_matmul_q_beam",
+           "bc_workspace_size_lora", "bc_beam_select", "bc_workspace_size_beam", "bc_matmul_q_beam",
            "bc_workspace_size_matmul_beam", "bc_beam_reorder",
            "bc_device_timeouts", "bc_set_wait_limit",
            "bc_status_string", "bc_version")
@@ -107,9 +107,11 @@ def _load() -> ctypes.CDLL:
     lib.bc_add_rmsnorm.argtypes = [P, i32, P, i32, P, i32, i64, i64, f32, P, i32, P]
     lib.bc_add_rmsnorm_q8.argtypes = [P, i32, P, i32, P, i32, i64, i64, f32, P, P, P, P]
     lib.bc_lora_add.argtypes = [P, i32, P, P, i32, i64, i64, i64, i64, i64, P, P, i64, P, P,
-                                P, P]
+                                P, P, sz, P]
     lib.bc_lora_add_batched.argtypes = [ctypes.POINTER(LoraDesc), i32, i64, i64, i64, i32, i32,
-                                        P, P, i64, P, P, P]
+                                        P, P, i64, P, P, P, sz, P]
+    lib.bc_workspace_size_lora.argtypes = [ctypes.POINTER(LoraDesc), i32, i64, i64, i64, i64]
+    lib.bc_workspace_size_lora.restype = sz
     lib.bc_beam_select.argtypes = [P, P, P, i64, i64, i64, i64, i32, i32, P, P, P, P, P, sz, P]
     lib.bc_workspace_size_beam.argtypes = [i64, i64, i64, i64]
     lib.bc_workspace_size_beam.restype = sz
@@ -503,9 +505,15 @@ def make_lora_descs(items: Sequence[tuple]) -> LoraDescs:
     return d
 
 
+def workspace_size_lora(descs: LoraDescs, n_segments: int) -> int:
+    return int(lib.bc_workspace_size_lora(descs.array, len(descs.array), descs.M, descs.R,
+                                          descs.n_adapters, n_segments))
+
+
 def lora_add_batched(descs: LoraDescs, seg_start: torch.Tensor, seg_adapter: torch.Tensor,
                      ranks: Optional[torch.Tensor] = None,
-                     scaling: Optional[torch.Tensor] = None, stream=None) -> None:
+                     scaling: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """y[m] += scaling[a] * B[a] (A[a] x[m]) for every projection of `descs`:
     the rows seg_start[i] .. seg_start[i+1]-1 use adapter a = seg_adapter[i]
     (outside 0..n_adapters-1: none).  seg_start int32 [S+1], seg_adapter int32
@@ -518,22 +526,27 @@ def lora_add_batched(descs: LoraDescs, seg_start: torch.Tensor, seg_adapter: tor
         _want(what, "ranks", ranks, (descs.n_adapters,), torch.int32)
     if scaling is not None:
         _want(what, "scaling", scaling, (descs.n_adapters,), torch.float32)
-    dev = _one_device(what, seg_start, seg_adapter, ranks, scaling)
+    dev = _one_device(what, seg_start, seg_adapter, ranks, scaling, workspace)
     if dev != descs.device:
         raise ValueError(f"{what}: all tensors must be on one device")
     with _Launch(what, dev, stream) as s:
+        if workspace is None:
+            workspace = torch.empty(workspace_size_lora(descs, S), dtype=torch.uint8, device=dev)
         _check(lib.bc_lora_add_batched(descs.array, len(descs.array), descs.M, descs.R,
                                        descs.n_adapters, descs.x_dtype, descs.w_dtype,
                                        seg_start.data_ptr(), seg_adapter.data_ptr(), S,
-                                       _p(ranks), _p(scaling), s), "bc_lora_add_batched")
+                                       _p(ranks), _p(scaling), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), s),
+               "bc_lora_add_batched")
 
 
 def lora_add(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, y: torch.Tensor,
              seg_start: torch.Tensor, seg_adapter: torch.Tensor,
              ranks: Optional[torch.Tensor] = None, scaling: Optional[torch.Tensor] = None,
-             stream=None) -> torch.Tensor:
+             workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """lora_add_batched for one projection; returns y."""
-    lora_add_batched(make_lora_descs([(x, A, B, y)]), seg_start, seg_adapter, ranks, scaling, stream)
+    lora_add_batched(make_lora_descs([(x, A, B, y)]), seg_start, seg_adapter, ranks, scaling,
+                     workspace, stream)
     return y
 
 

@@ -24,13 +24,13 @@ def _check(x, A, B, y0, y, start, adapter, ranks, scaling):
 
     Bound, relative to S = |c| sum_r (sum_k |A x|) |B|: an fp32 x, and v, enter
     as two tf32 pieces (2^-22 each); a tensor-core step of 8 products is taken
-    as 9 additions of 2^-23.  A warp takes 2 x 4 steps per 32 of the K / 256
-    that one of 8 x 8 warps has at most ceil(K / 2048) times; 15 additions join
-    the warps and blocks, one product brings the scale; ranks take 4 steps per
-    16.  Then y: one addition (2^-24 of the result)."""
+    as 9 additions of 2^-23.  Eight warps share K at least: 2 x 4 steps for each
+    of a warp's at most ceil(K / 256) pieces of 32; up to 8 + 16 additions join
+    the warps and the parts of K, one product brings the scale; ranks take 4
+    steps per 16.  Then y: one addition (2^-24 of the result)."""
     n, R, K = A.shape
-    steps1, steps2 = 8 * math.ceil(K / 2048), 4 * math.ceil(R / 16)
-    rel = 2 * 2.0 ** -22 + (9 * steps1 + 16 + 9 * steps2) * 2.0 ** -23
+    steps1, steps2 = 8 * math.ceil(K / 256), 4 * math.ceil(R / 16)
+    rel = 2 * 2.0 ** -22 + (9 * steps1 + 25 + 9 * steps2) * 2.0 ** -23
     seen = torch.zeros(x.shape[0], dtype=torch.bool)
     for i in range(len(adapter)):
         a, s0, s1 = int(adapter[i]), int(start[i]), int(start[i + 1])
@@ -159,7 +159,7 @@ def test_lora_rejects_on_host():
     import quantized_matmul_02_b200 as q
     at = [FAKE + (i << 26) for i in range(8)]
     ok = dict(x=at[0], xt=0, A=at[1], B=at[2], wt=1, M=4, N=32, K=64, R=8, n=2, start=at[3], adapter=at[4], S=4,
-              ranks=None, scaling=None, y=at[5], stream=None)
+              ranks=None, scaling=None, y=at[5], ws=at[6], wsb=1 << 20, stream=None)
     call = lambda **kw: q.lib.bc_lora_add(*{**ok, **kw}.values())  # noqa: E731
     for k in ("x", "A", "B", "start", "adapter", "y"):
         assert call(**{k: None}) == 1
@@ -168,10 +168,11 @@ def test_lora_rejects_on_host():
     assert call(K=96) == 1 and call(R=12) == 1 and call(R=136) == 2 and call(S=4097) == 2
     assert call(xt=1) == 2 and call(wt=0) == 2 and call(M=1 << 25) == 2 and call(N=1 << 30) == 2
     assert call(x=at[0] + 8) == 3 and call(A=at[1] + 2) == 3 and call(y=at[5] + 2) == 3 and call(start=at[3] + 1) == 3
+    assert call(ws=None) == 4 and call(wsb=64) == 4 and call(ws=at[6] + 8) == 3 and call(ws=at[5]) == 1
     assert call(y=at[0]) == 1 and call(y=at[2] + 64) == 1 and call(y=at[3]) == 1
     arr = (q.LoraDesc * 2)(*[q.LoraDesc(at[0], at[1], at[2], at[5], 32, 64)] * 2)
-    assert q.lib.bc_lora_add_batched(arr, 2, 4, 8, 2, 0, 1, at[3], at[4], 4, None, None, None) == 1   # one y twice
-    assert q.lib.bc_lora_add_batched(None, 1, 4, 8, 2, 0, 1, at[3], at[4], 4, None, None, None) == 1
+    assert q.lib.bc_lora_add_batched(arr, 2, 4, 8, 2, 0, 1, at[3], at[4], 4, None, None, at[6], 1 << 20, None) == 1   # one y twice
+    assert q.lib.bc_lora_add_batched(None, 1, 4, 8, 2, 0, 1, at[3], at[4], 4, None, None, at[6], 1 << 20, None) == 1
     with pytest.raises(ValueError):
         q.make_lora_descs([(torch.zeros(2, 64), torch.zeros(1, 8, 64).half(), torch.zeros(1, 4, 8).half(), torch.zeros(2, 4))])
     with pytest.raises(ValueError):
