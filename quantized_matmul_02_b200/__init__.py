@@ -110,7 +110,7 @@ def _load() -> ctypes.CDLL:
                                 P, P, sz, P]
     lib.bc_lora_add_batched.argtypes = [ctypes.POINTER(LoraDesc), i32, i64, i64, i64, i32, i32,
                                         P, P, i64, P, P, P, sz, P]
-    lib.bc_workspace_size_lora.argtypes = [ctypes.POINTER(LoraDesc), i32, i64, i64, i64, i64]
+    lib.bc_workspace_size_lora.argtypes = [ctypes.POINTER(LoraDesc), i32, i64, i64, i64, i64, i32]
     lib.bc_workspace_size_lora.restype = sz
     lib.bc_beam_select.argtypes = [P, P, P, i64, i64, i64, i64, i32, i32, P, P, P, P, P, sz, P]
     lib.bc_workspace_size_beam.argtypes = [i64, i64, i64, i64]
@@ -507,7 +507,7 @@ def make_lora_descs(items: Sequence[tuple]) -> LoraDescs:
 
 def workspace_size_lora(descs: LoraDescs, n_segments: int) -> int:
     return int(lib.bc_workspace_size_lora(descs.array, len(descs.array), descs.M, descs.R,
-                                          descs.n_adapters, n_segments))
+                                          descs.n_adapters, n_segments, descs.x_dtype))
 
 
 def lora_add_batched(descs: LoraDescs, seg_start: torch.Tensor, seg_adapter: torch.Tensor,

@@ -5,13 +5,14 @@
 //   ranks of R in use.
 //
 // Two launches for a whole set of projections.  Rows that share an adapter
-// are cut into tiles.  shrink_kernel forms v = A x, a block per (tile,
-// projection, 32 ranks, part of K), and leaves its partial sums in scratch;
-// expand_kernel joins the parts and adds B v, a block per (tile, projection,
-// range of columns).  x, A, B and y go between global memory and matrix
-// fragments directly: the order of the contraction index is free, so a lane
-// takes 16-byte pieces along it, and y's columns are dealt to the fragments
-// so that a lane holds eight neighbours.
+// are cut into tiles.  shrink_kernel forms c A x, a cluster per (tile, 32 ranks
+// of the projections that read the same x), its blocks sharing K and joining
+// their sums through distributed shared memory; it leaves them in scratch, in
+// the order of expand_kernel's fragments.  expand_kernel adds B v, a block per
+// (16 rows, 256 columns).  x, A, B, v and y go between global memory and
+// matrix fragments directly: the order of the contraction index is free, so a
+// lane takes 16-byte pieces along it, and y's columns are dealt to the
+// fragments so that lanes side by side hold whole sectors.
 //
 // What bounds it: the bytes of y (fp32, read and written) and x for prompts,
 // the bytes of the adapters for single tokens; 2 R (K + N) operations a row
@@ -23,10 +24,14 @@
 // Sums run in a fixed order: results do not change from call to call.
 #include "bc_internal.cuh"
 
+#include <cooperative_groups.h>
+
 #include <type_traits>
 
 namespace bc {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -36,16 +41,17 @@ constexpr int kMaxSegments = 4096;
 constexpr int kMaxRank = 128;
 constexpr int kGroupRows = 256;        // up to here rows are ordered by adapter
 constexpr int kChunk = 32;             // ranks per shrink block
-constexpr int kMaxSplit = 16;          // parts of K
-constexpr int kUnits = 4;              // 32-column steps per warp of an expand block
-constexpr int kCols = kUnits * kWarps * 32;
+constexpr int kMaxSplit = 8;           // parts of K (blocks of a cluster)
+constexpr int kStep = kWarps * 32;     // columns an expand block takes at a time
+constexpr int kMaxSteps = 12;          // such steps per block
+constexpr int kStages = 3;             // of which y is on its way
 
 struct Desc {
     const void *x, *A, *B;
     float *y;
     int N, K;
-    int split;                         // parts of K
-    int first_block;                   // expand: first of this projection's column ranges
+    int group_size;                    // at a group's first projection: how many read its x
+    int first_block, blocks;           // expand: this projection's column blocks
 };
 // A tile: `rows` rows of `adapter`.  Row i is first + i, or order[first + i].
 struct Tile {
@@ -59,12 +65,13 @@ struct LoraArgs {
     const float *scaling;              // [adapters] or null
     int64_t M;
     int S, R, adapters, count;
-    int max_tiles;
-    int col_blocks;                    // column ranges of all projections
-    int split;                         // largest of the projections'
-    int *head;                         // scratch: [0] tiles, [1..] order of the rows (grouped)
-    Tile *tiles;                       // scratch: [max_tiles]
-    float *v;                          // scratch: [count][max_tiles][split][T * R16], fragment order
+    int T, max_tiles;
+    int col_blocks, steps;             // column blocks of all projections, their steps
+    int split;                         // parts of K
+    int chunks;                        // 32-rank chunks of all groups
+    int *head;                         // scratch: the rows' order (grouped)
+    Tile *tiles;                       // scratch: [max_tiles], rows = 0 where unused
+    float4 *v;                         // scratch: [count][max_tiles][MB][R16 / 16][2][32]
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -98,18 +105,14 @@ __device__ __forceinline__ void widen(uint32_t u, uint32_t &a, uint32_t &b) {
     }
 }
 
-// Row stride of v in shared memory, in floats: 16 modulo 32 keeps the eight
-// lanes of a 16-byte load phase (two rows, 64 bytes each) off each other's banks.
-__host__ __device__ __forceinline__ int v_stride(int R16) { return R16 | 16; }
-
-
 // The tile table.  Few rows (decode): rows are ordered by adapter, so that
 // requests of one adapter share its reads.  More rows: every segment is cut as
 // it stands.  Each shrink block works it out for itself (a few hundred cycles
 // for decode) and keeps only its own tile; the first block of a tile leaves
-// it for expand_kernel, block 0 the number of tiles and the rows' order.
+// it for expand_kernel, block 0 the rows' order.
 struct PlanShared {
-    int key[kGroupRows], order[kGroupRows], scan[kWarps + 1];
+    __align__(16) int key[kGroupRows];
+    int order[kGroupRows], scan[kWarps + 1];
     Tile mine;
     int found;
 };
@@ -141,11 +144,15 @@ __device__ __forceinline__ void plan(const LoraArgs &a, PlanShared &p, int want,
         __syncthreads();
         const int mine = p.key[tid];
         int before = 0, same = 0, all = 0;
-        for (int j = 0; j < M; ++j) {
-            const int k = p.key[j];
-            before += k < mine;
-            same += k == mine && j < tid;
-            all += k == mine;
+        for (int j = 0; j < M; j += 4) {         // places behind M hold kNone
+            const int4 q = *reinterpret_cast<const int4 *>(p.key + j);
+            const int k[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                before += k[e] < mine;
+                same += k[e] == mine && j + e < tid;
+                all += k[e] == mine;
+            }
         }
         before += same;
         const bool live = tid < M && mine != kNone, head = live && same % T == 0;
@@ -159,11 +166,8 @@ __device__ __forceinline__ void plan(const LoraArgs &a, PlanShared &p, int want,
         const unsigned heads = __ballot_sync(0xffffffffu, p.key[tid] >= 0);
         if (lane == 0) p.scan[warp] = __popc(heads);
         __syncthreads();
-        int base = 0, total = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) base += p.scan[w];
-            total += p.scan[w];
-        }
+        int base = 0;
+        for (int w = 0; w < warp; ++w) base += p.scan[w];
         const int owner = p.key[tid];
         const int at = base + __popc(heads & ((1u << lane) - 1));
         __syncthreads();
@@ -178,8 +182,7 @@ __device__ __forceinline__ void plan(const LoraArgs &a, PlanShared &p, int want,
             }
         }
         if (publish) {
-            if (tid < M) a.head[1 + tid] = p.order[tid];
-            if (tid == 0) a.head[0] = total;
+            if (tid < M) a.head[tid] = p.order[tid];
         }
         __syncthreads();
         return;
@@ -200,11 +203,8 @@ __device__ __forceinline__ void plan(const LoraArgs &a, PlanShared &p, int want,
     }
     if (lane == 31) p.scan[warp] = inc;
     __syncthreads();
-    int at = inc - own, total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) at += p.scan[w];
-        total += p.scan[w];
-    }
+    int at = inc - own;
+    for (int w = 0; w < warp; ++w) at += p.scan[w];
     for (int i = i0; i < i1; ++i) {
         const int n = tiles_in(i, s0, s1);
         if (want >= at && want < at + n) {
@@ -214,66 +214,79 @@ __device__ __forceinline__ void plan(const LoraArgs &a, PlanShared &p, int want,
         }
         at += n;
     }
-    if (publish && tid == 0) a.head[0] = total;
     __syncthreads();
 }
 
-// grid: tiles x projections x rank chunks x parts of K
+// grid: tiles x rank chunks x parts of K; a cluster is the parts of one K
 template <typename X, typename W, int MB>
 __global__ void __launch_bounds__(kThreads, 2)
 shrink_kernel(const __grid_constant__ LoraArgs a) {
-    constexpr int T = 16 * MB;
+    constexpr int T = 16 * MB, NB = kChunk / 8;
     constexpr bool kBf16 = std::is_same<X, __nv_bfloat16>::value && std::is_same<W, __nv_bfloat16>::value;
     constexpr bool kF32 = std::is_same<X, float>::value;
+    constexpr int kQ = kF32 ? 2 : 1;                           // 16-byte pieces of a lane's eight x
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     __shared__ PlanShared ps;
-    __shared__ __align__(16) float red[kWarps * T * kChunk];
-    const int chunks = (a.R + kChunk - 1) / kChunk;
-    const int per_tile = a.count * chunks * a.split;
+    __shared__ __align__(16) float4 red[kWarps * T * kChunk / 4];
+    const int per_tile = a.chunks * a.split;
     const int ti = blockIdx.x / per_tile, inner = blockIdx.x - ti * per_tile;
-    const int part = inner % a.split, chunk = inner / a.split % chunks, di = inner / a.split / chunks;
+    const int part = inner % a.split;
+    int chunk = inner / a.split;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     plan<T>(a, ps, ti, blockIdx.x == 0);
-    if (!ps.found) return;
-    const Tile tile = ps.mine;
+    const Tile tile = ps.found ? ps.mine : Tile{0, 0, 0, 0};
     if (inner == 0 && tid == 0) a.tiles[ti] = tile;
-    const Desc &d = a.d[di];
-    if (part >= d.split) return;
-    const int K = d.K, R = a.R, R16 = (R + 15) / 16 * 16, r0 = chunk * kChunk, n_rows = tile.rows;
-    const int rank = a.ranks ? min(a.ranks[tile.adapter], R) : R;
-    if (r0 >= rank) return;
-    const bool grouped = a.M <= kGroupRows;
-    int64_t row[MB][2];
+    if (!ps.found) return;                                     // (the whole cluster)
+    // the chunk's projections: blocks of eight ranks of all that read one x, in a row
+    const int R = a.R, R8 = R / 8, R16 = (R + 15) / 16 * 16, n_rows = tile.rows;
+    int first = 0;
+    while (chunk >= (a.d[first].group_size * R8 + NB - 1) / NB) {
+        chunk -= (a.d[first].group_size * R8 + NB - 1) / NB;
+        first += a.d[first].group_size;
+    }
+    const int K = a.d[first].K, blocks = a.d[first].group_size * R8;
+    const int rank = a.ranks ? min(a.ranks[tile.adapter], R) : R, used = (rank + 7) / 8;
+    const float scale = a.scaling ? a.scaling[tile.adapter] : 1.f;
+    const W *arow[NB];                                         // this lane's row of A, or null
+    unsigned live = 0;                                         // blocks that have ranks
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int vb = chunk * NB + b, rb = vb % R8, r = rb * 8 + g;
+        arow[b] = nullptr;
+        if (vb < blocks && rb < used) {
+            live |= 1u << b;
+            if (r < rank)
+                arow[b] = static_cast<const W *>(a.d[first + vb / R8].A) + ((int64_t)tile.adapter * R + r) * K + t * 8;
+        }
+    }
+    if (!live) return;                                          // (the whole cluster)
+    const X *xrow[MB][2];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i = mb * 16 + g + h * 8;
-            row[mb][h] = i >= n_rows ? -1 : grouped ? ps.order[tile.first + i] : tile.first + i;
+            xrow[mb][h] = nullptr;
+            if (i < n_rows) {
+                const int64_t m = a.M <= kGroupRows ? ps.order[tile.first + i] : tile.first + i;
+                xrow[mb][h] = static_cast<const X *>(a.d[first].x) + m * K + t * 8;
+            }
         }
-    const int nb = min(kChunk, rank - r0 + 7) / 8;             // blocks of eight ranks
-    const W *A = static_cast<const W *>(d.A) + (int64_t)tile.adapter * R * K;
-    float acc[MB][kChunk / 8][4] = {};
-    for (int u = part * kWarps + warp; u < K / 32; u += d.split * kWarps) {
-        const int k = u * 32 + t * 8;
-        uint4 wa[kChunk / 8];
+    auto load = [&](int u, uint4 (&wa)[NB], uint4 (&xa)[MB][2][kQ]) {
 #pragma unroll
-        for (int b = 0; b < kChunk / 8; ++b) {
-            const int r = r0 + b * 8 + g;
-            wa[b] = make_uint4(0, 0, 0, 0);
-            if (b < nb && r < rank) wa[b] = *reinterpret_cast<const uint4 *>(A + (int64_t)r * K + k);
-        }
-        uint4 xa[MB][2][kF32 ? 2 : 1];
+        for (int b = 0; b < NB; ++b)
+            wa[b] = arow[b] ? *reinterpret_cast<const uint4 *>(arow[b] + u * 32) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4 *p = reinterpret_cast<const uint4 *>(
-                    static_cast<const X *>(d.x) + row[mb][h] * K + k);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int q = 0; q < (kF32 ? 2 : 1); ++q)
-                    xa[mb][h][q] = row[mb][h] >= 0 ? p[q] : make_uint4(0, 0, 0, 0);
-            }
+                for (int q = 0; q < kQ; ++q)
+                    xa[mb][h][q] = xrow[mb][h] ? reinterpret_cast<const uint4 *>(xrow[mb][h] + u * 32)[q]
+                                               : make_uint4(0, 0, 0, 0);
+    };
+    float acc[MB][NB][4] = {};
+    auto multiply = [&](const uint4 (&wa)[NB], const uint4 (&xa)[MB][2][kQ]) {
         if constexpr (kBf16) {
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
@@ -284,7 +297,7 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
                     const uint32_t f[4] = {s ? p.z : p.x, s ? q.z : q.x, s ? p.w : p.y, s ? q.w : q.y};
 #pragma unroll
                     for (int b = 0; b < kChunk / 8; ++b)
-                        if (b < nb) mma_bf16(acc[mb][b], f, s ? wa[b].z : wa[b].x, s ? wa[b].w : wa[b].y);
+                        if (live >> b & 1) mma_bf16(acc[mb][b], f, s ? wa[b].z : wa[b].x, s ? wa[b].w : wa[b].y);
                 }
             }
         } else {
@@ -311,7 +324,7 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
                     }
 #pragma unroll
                     for (int b = 0; b < kChunk / 8; ++b)
-                        if (b < nb) {
+                        if (live >> b & 1) {
                             if constexpr (kF32)
                                 mma_tf32(acc[mb][b], lo[0], lo[1], lo[2], lo[3], w0[b], w1[b]);
                             mma_tf32(acc[mb][b], hi[0], hi[1], hi[2], hi[3], w0[b], w1[b]);
@@ -319,227 +332,237 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
                 }
             }
         }
+    };
+    // the next step's pieces are on their way while this one's are multiplied
+    uint4 wa[2][NB], xa[2][MB][2][kQ];
+    const int step = a.split * kWarps, units = K / 32;
+    int u = part * kWarps + warp;
+    if (u < units) load(u, wa[0], xa[0]);
+    for (; u < units; u += 2 * step) {
+        if (u + step < units) load(u + step, wa[1], xa[1]);
+        multiply(wa[0], xa[0]);
+        if (u + step < units) {
+            if (u + 2 * step < units) load(u + 2 * step, wa[0], xa[0]);
+            multiply(wa[1], xa[1]);
+        }
     }
     // the block's sum over its warps, in fragment order
-    float4 *mine = reinterpret_cast<float4 *>(red) + warp * (T * kChunk / 4);
+    constexpr int kQuads = T * kChunk / 4;
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-        for (int b = 0; b < kChunk / 8; ++b)
-            mine[(mb * (kChunk / 8) + b) * 32 + lane] =
+        for (int b = 0; b < NB; ++b)
+            red[warp * kQuads + (mb * NB + b) * 32 + lane] =
                 make_float4(acc[mb][b][0], acc[mb][b][1], acc[mb][b][2], acc[mb][b][3]);
     __syncthreads();
-    float4 *out = reinterpret_cast<float4 *>(
-        a.v + (((int64_t)di * a.max_tiles + ti) * a.split + part) * (T * R16));
-    for (int i = tid; i < T * kChunk / 4; i += kThreads) {
-        const int mb = i / 32 / (kChunk / 8), b = i / 32 % (kChunk / 8);
-        if (b >= nb || mb * 16 >= n_rows) continue;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = tid; i < kQuads; i += kThreads) {
+        float4 s = red[i];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float4 p = reinterpret_cast<const float4 *>(red)[w * (T * kChunk / 4) + i];
+        for (int w = 1; w < kWarps; ++w) {
+            const float4 p = red[w * kQuads + i];
             s.x += p.x;
             s.y += p.y;
             s.z += p.z;
             s.w += p.w;
         }
-        out[(mb * (R16 / 8) + r0 / 8 + b) * 32 + (i & 31)] = s;
+        red[i] = s;
     }
+    // the cluster's sum: every block takes a share of the places
+    cg::cluster_group cluster = cg::this_cluster();
+    if (a.split > 1) cluster.sync();
+    else __syncthreads();
+    for (int i = part * kThreads + tid; i < kQuads; i += a.split * kThreads) {
+        const int mb = i / 32 / NB, vb = chunk * NB + i / 32 % NB, rb = vb % R8;
+        if (vb >= blocks || rb >= used || mb * 16 >= n_rows) continue;
+        float4 s = red[i];
+        if (a.split > 1) {
+            s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < a.split; ++c) {
+                const float4 p = cluster.map_shared_rank(red, c)[i];
+                s.x += p.x;
+                s.y += p.y;
+                s.z += p.z;
+                s.w += p.w;
+            }
+        }
+        // ranks rb * 8 + 2 t and the next, of rows g and g + 8: half of a lane's four ranks there
+        const int l = i & 31, q = rb / 2, lq = (rb & 1) * 2 + (l & 3) / 2;
+        float2 *out = reinterpret_cast<float2 *>(
+            a.v + ((((int64_t)(first + vb / R8) * a.max_tiles + ti) * MB + mb) * (R16 / 16) + q) * 64 +
+            (l >> 2) * 4 + lq) + (l & 1);
+        out[0] = make_float2(s.x * scale, s.y * scale);
+        out[64] = make_float2(s.z * scale, s.w * scale);
+    }
+    if (a.split > 1) cluster.sync();                           // the others may still read this block's sums
 }
 
-// grid: tiles x column ranges of all projections
+__device__ __forceinline__ void copy16(float4 *to, const float *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+                 : "memory");
+}
+
+// grid: tiles x MB x column blocks of all projections
 template <typename W, int MB>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
 expand_kernel(const __grid_constant__ LoraArgs a) {
-    constexpr int T = 16 * MB;
+    // each lane's own pieces of y, loaded two steps ahead: only their owner touches them
+    __shared__ __align__(16) float4 ring[kWarps][kStages][4][32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int R = a.R, R16 = (R + 15) / 16 * 16, VS = v_stride(R16);
-    extern __shared__ __align__(16) float vsm[];
-    float *vhi = vsm, *vlo = vsm + T * VS;                     // [T][VS]
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int ti = blockIdx.x / a.col_blocks, cb = blockIdx.x - ti * a.col_blocks;
-    if (ti >= a.head[0]) return;
-    const Tile tile = a.tiles[ti];
+    const int sub = blockIdx.x / a.col_blocks, cb = blockIdx.x - sub * a.col_blocks;
+    const int ti = sub / MB, mb = sub - ti * MB;
     int di = 0;
     while (di + 1 < a.count && cb >= a.d[di + 1].first_block) ++di;
     const Desc &d = a.d[di];
-    const int N = d.N, n_rows = tile.rows;
-    const int rank = a.ranks ? min(a.ranks[tile.adapter], R) : R, used = (rank + 7) / 8;
-    const float scale = a.scaling ? a.scaling[tile.adapter] : 1.f;
-    const bool grouped = a.M <= kGroupRows;
-    int64_t row[MB][2];
+    const int N = d.N, R = a.R, R16 = (R + 15) / 16 * 16;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Tile tile = a.tiles[ti];
+    if (mb * 16 >= tile.rows) return;
+    float *yrow[2];
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = mb * 16 + g + h * 8;
-            row[mb][h] = i >= n_rows ? -1 : grouped ? a.head[1 + tile.first + i] : tile.first + i;
+    for (int h = 0; h < 2; ++h) {
+        const int i = mb * 16 + g + h * 8;
+        yrow[h] = nullptr;
+        if (i < tile.rows) {
+            const int64_t m = a.M <= kGroupRows ? a.head[tile.first + i] : tile.first + i;
+            yrow[h] = d.y + m * N;
         }
-    const W *B = static_cast<const W *>(d.B) + (int64_t)tile.adapter * R * N;
-
-    // v of the tile: the parts' sum, as two tf32 pieces
-    const float4 *in = reinterpret_cast<const float4 *>(
-        a.v + ((int64_t)di * a.max_tiles + ti) * a.split * (T * R16));
-    for (int i = tid; i < T * R16 / 4; i += kThreads) {
-        const int b = i / 32 % (R16 / 8), l = i & 31, m = i / 32 / (R16 / 8) * 16 + (l >> 2);
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (b < used && m < n_rows)
-            for (int p = 0; p < d.split; ++p) {
-                const float4 q = in[p * (T * R16 / 4) + i];
-                s.x += q.x;
-                s.y += q.y;
-                s.z += q.z;
-                s.w += q.w;
-            }
-        const float f[4] = {s.x * scale, s.y * scale, s.z * scale, s.w * scale};
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split_tf32(f[e], hi[e], lo[e]);
-        uint2 *h = reinterpret_cast<uint2 *>(vhi + m * VS + b * 8 + (l & 3) * 2);
-        uint2 *o = reinterpret_cast<uint2 *>(vlo + m * VS + b * 8 + (l & 3) * 2);
-        h[0] = make_uint2(hi[0], hi[1]);
-        h[4 * VS] = make_uint2(hi[2], hi[3]);
-        o[0] = make_uint2(lo[0], lo[1]);
-        o[4 * VS] = make_uint2(lo[2], lo[3]);
     }
-    __syncthreads();
-
-    // y += B v, 32 columns a warp and step: column 2 t + i of block j is
-    // column t * 8 + j * 2 + i of the 32
     const bool vec = (N & 3) == 0 && (reinterpret_cast<uintptr_t>(d.y) & 15) == 0;
-    const int c0 = (cb - d.first_block) * kCols;
-    for (int s = 0; s < kUnits; ++s) {
-        const int n0 = c0 + (s * kWarps + warp) * 32, nc = n0 + t * 8;
+    // a block's steps lie apart, so that blocks side by side run over
+    // neighbouring columns: step s covers the warp's 32 columns from here
+    auto column = [&](int s) { return ((s * d.blocks + cb - d.first_block) * kWarps + warp) * 32; };
+    auto prefetch = [&](int s) {
+        const int nc = column(s) + t * 4;
+        if (vec && s < a.steps) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (yrow[h] && nc + q * 16 < N) copy16(&ring[warp][s % kStages][h * 2 + q][lane], yrow[h] + nc + q * 16);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    prefetch(0);
+    prefetch(1);
+    const int rank = a.ranks ? min(a.ranks[tile.adapter], R) : R, used = (rank + 7) / 8 * 8;
+    const W *B = static_cast<const W *>(d.B) + (int64_t)tile.adapter * R * N;
+    const float4 *v = a.v + (((int64_t)di * a.max_tiles + ti) * MB + mb) * (R16 / 16) * 64 + lane;
+    for (int s = 0; s < a.steps; ++s) {
+        const int n0 = column(s), nc = n0 + t * 4;
         if (n0 >= N) break;
-        float acc[MB][4][4] = {};                          // [block of rows][j][fragment]
-        float yv[MB][2][8];                                // the outputs so far, loaded before the products
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (row[mb][h] < 0) continue;
-                const float *p = d.y + row[mb][h] * N + nc;
-                if (vec) {
-#pragma unroll
-                    for (int q = 0; q < 8; q += 4)
-                        if (nc + q < N) {
-                            const float4 f = *reinterpret_cast<const float4 *>(p + q);
-                            yv[mb][h][q] = f.x;
-                            yv[mb][h][q + 1] = f.y;
-                            yv[mb][h][q + 2] = f.z;
-                            yv[mb][h][q + 3] = f.w;
-                        }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (nc + q < N) yv[mb][h][q] = p[q];
-                }
-            }
+        prefetch(s + 2);
+        // y += B v: column 2 t + i of block j is column j / 2 * 16 + t * 4 + j % 2 * 2 + i of
+        // the 32, so that a lane holds 4 neighbours twice and 4 lanes whole sectors
+        float acc[4][4] = {};                                  // [j][fragment]
         for (int r0 = 0; r0 < rank; r0 += 16) {
             const int r = r0 + t * 4;
-            uint32_t w[4][4];                              // [j][the lane's four ranks]
+            float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
+            if (r < used) {
+                v0 = v[r0 * 4];
+                v1 = v[r0 * 4 + 32];
+            }
+            uint32_t w[4][4];                                  // [j][the lane's four ranks]
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int n = n0 + (g >> 1) * 8 + j * 2 + (g & 1);
+                const int n = n0 + (j >> 1) * 16 + (g >> 1) * 4 + (j & 1) * 2 + (g & 1);
                 uint2 q = make_uint2(0, 0);
                 if (n < N && r < rank) q = *reinterpret_cast<const uint2 *>(B + (int64_t)n * R + r);
                 widen<W>(q.x, w[j][0], w[j][1]);
                 widen<W>(q.y, w[j][2], w[j][3]);
 #pragma unroll
                 for (int e = 1; e < 4; ++e)
-                    if (r + e >= rank) w[j][e] = 0;        // behind the adapter's rank: not its values
+                    if (r + e >= rank) w[j][e] = 0;            // behind the adapter's rank: not its values
             }
+            uint32_t h0[4], h1[4], l0[4], l1[4];
+            split_tf32(v0.x, h0[0], l0[0]);
+            split_tf32(v0.y, h0[1], l0[1]);
+            split_tf32(v0.z, h0[2], l0[2]);
+            split_tf32(v0.w, h0[3], l0[3]);
+            split_tf32(v1.x, h1[0], l1[0]);
+            split_tf32(v1.y, h1[1], l1[1]);
+            split_tf32(v1.z, h1[2], l1[2]);
+            split_tf32(v1.w, h1[3], l1[3]);
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb) {
-                if (mb * 16 >= n_rows) break;
-                const int at = (mb * 16 + g) * VS + r;
-                const uint4 h0 = *reinterpret_cast<const uint4 *>(vhi + at);
-                const uint4 h1 = *reinterpret_cast<const uint4 *>(vhi + at + 8 * VS);
-                const uint4 l0 = *reinterpret_cast<const uint4 *>(vlo + at);
-                const uint4 l1 = *reinterpret_cast<const uint4 *>(vlo + at + 8 * VS);
+            for (int j = 0; j < 4; ++j) {
+                mma_tf32(acc[j], l0[0], l1[0], l0[1], l1[1], w[j][0], w[j][1]);
+                mma_tf32(acc[j], l0[2], l1[2], l0[3], l1[3], w[j][2], w[j][3]);
+                mma_tf32(acc[j], h0[0], h1[0], h0[1], h1[1], w[j][0], w[j][1]);
+                mma_tf32(acc[j], h0[2], h1[2], h0[3], h1[3], w[j][2], w[j][3]);
+            }
+        }
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    mma_tf32(acc[mb][j], l0.x, l1.x, l0.y, l1.y, w[j][0], w[j][1]);
-                    mma_tf32(acc[mb][j], l0.z, l1.z, l0.w, l1.w, w[j][2], w[j][3]);
-                    mma_tf32(acc[mb][j], h0.x, h1.x, h0.y, h1.y, w[j][0], w[j][1]);
-                    mma_tf32(acc[mb][j], h0.z, h1.z, h0.w, h1.w, w[j][2], w[j][3]);
+        for (int h = 0; h < 2; ++h) {
+            if (!yrow[h]) continue;
+            float *p = yrow[h] + nc;
+            if (vec) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (nc + q * 16 < N) {
+                        float4 f = ring[warp][s % kStages][h * 2 + q][lane];
+                        f.x += acc[q * 2][h * 2];
+                        f.y += acc[q * 2][h * 2 + 1];
+                        f.z += acc[q * 2 + 1][h * 2];
+                        f.w += acc[q * 2 + 1][h * 2 + 1];
+                        *reinterpret_cast<float4 *>(p + q * 16) = f;
+                    }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int c = (q >> 2) * 16 + (q & 3);
+                    if (nc + c < N) p[c] += acc[q >> 1][h * 2 + (q & 1)];
                 }
             }
         }
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (row[mb][h] < 0) continue;
-                float *p = d.y + row[mb][h] * N + nc;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) yv[mb][h][q] += acc[mb][q >> 1][h * 2 + (q & 1)];
-                if (vec) {
-#pragma unroll
-                    for (int q = 0; q < 8; q += 4)
-                        if (nc + q < N)
-                            *reinterpret_cast<float4 *>(p + q) = make_float4(
-                                yv[mb][h][q], yv[mb][h][q + 1], yv[mb][h][q + 2], yv[mb][h][q + 3]);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (nc + q < N) p[q] = yv[mb][h][q];
-                }
-            }
     }
 }
 
-// Tile height: 16 rows while rows are few or segments short, else 32.
-int tile_rows(int64_t M, int64_t S) { return M <= kGroupRows || M / S <= 16 ? 16 : 32; }
+// Tile height: 16 rows while rows are few or segments short, else 32; fp32
+// rows take 16 (two pieces of 32 would not fit the registers).
+int tile_rows(int64_t M, int64_t S, bool f32) { return f32 || M <= kGroupRows || M / S <= 16 ? 16 : 32; }
 // At most this many tiles: full ones, and a ragged one per segment (or adapter).
-int64_t most_tiles(int64_t M, int64_t S, int64_t adapters) {
-    const int64_t T = tile_rows(M, S);
+int64_t most_tiles(int64_t M, int64_t S, int64_t adapters, int64_t T) {
     const int64_t ragged = M <= kGroupRows && adapters < S ? adapters : S;
     return M / T + (ragged < M ? ragged : M);
 }
-// Parts of K for `blocks` blocks per part: enough blocks to fill the GPU
-// about three times, a step of 32 for every warp at least.
-int split_of(int64_t K, int64_t blocks) {
-    int64_t s = (3 * kSms + blocks - 1) / blocks;
-    const int64_t most = (K / 32 + kWarps - 1) / kWarps;
-    s = s < most ? s : most;
-    return (int)(s < 1 ? 1 : s > kMaxSplit ? kMaxSplit : s);
+// Steps of an expand block: one while that does not fill the GPU, more to
+// share a block's start among its columns.
+int steps_of(const bc_lora_desc *descs, int count, int64_t row_tiles) {
+    int64_t all = 0;
+    for (int i = 0; i < count; ++i) all += (descs[i].N + kStep - 1) / kStep;
+    const int64_t s = all * row_tiles / (4 * kSms);
+    return (int)(s < 1 ? 1 : s > kMaxSteps ? kMaxSteps : s);
 }
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Scratch of one launch over `count` projections, and the launch's split.
-size_t scratch(const bc_lora_desc *descs, int count, int64_t M, int64_t R, int64_t adapters,
-               int64_t S, int *split) {
-    const int64_t T = tile_rows(M, S), tiles = most_tiles(M, S, adapters), R16 = (R + 15) / 16 * 16;
-    const int64_t blocks = tiles * count * ((R + kChunk - 1) / kChunk);
-    int most = 1;
-    for (int i = 0; i < count; ++i) {
-        const int s = split_of(descs[i].K, blocks);
-        most = s > most ? s : most;
-    }
-    *split = most;
-    return round256((size_t)(1 + kGroupRows) * 4) + round256((size_t)tiles * sizeof(Tile)) +
-           (size_t)count * tiles * most * T * R16 * 4;
+// Scratch of one launch over `count` projections.
+size_t scratch(int count, int64_t M, int64_t R, int64_t adapters, int64_t S, bool f32) {
+    const int64_t T = tile_rows(M, S, f32), tiles = most_tiles(M, S, adapters, T), R16 = (R + 15) / 16 * 16;
+    return round256((size_t)kGroupRows * 4) + round256((size_t)tiles * sizeof(Tile)) +
+           (size_t)count * tiles * T * R16 * 4;
 }
 
 template <typename X, typename W, int MB>
 bc_status launch(const LoraArgs &a, cudaStream_t s) {
-    const int chunks = (a.R + kChunk - 1) / kChunk, R16 = (a.R + 15) / 16 * 16;
-    const size_t smem = (size_t)2 * 16 * MB * v_stride(R16) * 4;
-    shrink_kernel<X, W, MB><<<(unsigned)(a.max_tiles * a.count * chunks * a.split), kThreads, 0, s>>>(a);
-    bc_status st = cuda_status();
-    if (st != BC_OK) return st;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.max_tiles * a.col_blocks));
+    cfg.gridDim = dim3((unsigned)(a.max_tiles * a.chunks * a.split));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = a.split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, expand_kernel<W, MB>, a) != cudaSuccess) {
+    cudaError_t e = cudaLaunchKernelEx(&cfg, shrink_kernel<X, W, MB>, a);
+    if (e == cudaSuccess) {
+        // expand's blocks may start while shrink's finish; they wait for all of it before they read
+        cfg.gridDim = dim3((unsigned)(a.max_tiles * MB * a.col_blocks));
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        e = cudaLaunchKernelEx(&cfg, expand_kernel<W, MB>, a);
+    }
+    if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return BC_ERR_CUDA;
     }
@@ -548,7 +571,9 @@ bc_status launch(const LoraArgs &a, cudaStream_t s) {
 
 template <typename X, typename W>
 bc_status launch(const LoraArgs &a, cudaStream_t s) {
-    return tile_rows(a.M, a.S) == 16 ? launch<X, W, 1>(a, s) : launch<X, W, 2>(a, s);
+    if constexpr (!std::is_same<X, float>::value)
+        if (a.T == 32) return launch<X, W, 2>(a, s);
+    return launch<X, W, 1>(a, s);
 }
 
 bool overlap(const void *p, size_t pn, const void *q, size_t qn) {
@@ -564,13 +589,13 @@ bool sizes_ok(const bc_lora_desc *descs, int count, int64_t M, int64_t R, int64_
         if (descs[i].N <= 0 || descs[i].K <= 0 || descs[i].K % 64) return false;
     *st = BC_ERR_UNSUPPORTED;
     if (M > (int64_t)1 << 24 || n_segments > kMaxSegments || n_adapters > 1 << 20 || R > kMaxRank) return false;
-    const int64_t tiles = most_tiles(M, n_segments, n_adapters);
+    const int64_t tiles = most_tiles(M, n_segments, n_adapters, 16);       // the most there can be
     for (int i = 0; i < count; i += kMaxDescs) {
         const int n = count - i < kMaxDescs ? count - i : kMaxDescs;
         int64_t cols = 0;
         for (int j = 0; j < n; ++j) {
             if (descs[i + j].N >= (int64_t)1 << 30 || descs[i + j].K >= (int64_t)1 << 24) return false;
-            cols += (descs[i + j].N + kCols - 1) / kCols;
+            cols += (descs[i + j].N + kStep - 1) / kStep;
         }
         // blocks of one launch
         if (tiles * cols >= (int64_t)1 << 31) return false;
@@ -588,17 +613,11 @@ using namespace bc;
 extern "C" {
 
 size_t bc_workspace_size_lora(const bc_lora_desc *descs, int count, int64_t M, int64_t R,
-                              int64_t n_adapters, int64_t n_segments) {
+                              int64_t n_adapters, int64_t n_segments, bc_dtype x_dtype) {
     bc_status st;
     if (!sizes_ok(descs, count, M, R, n_adapters, n_segments, &st)) return 0;
-    size_t most = 0;
-    for (int i = 0; i < count; i += kMaxDescs) {           // launches use the scratch in turn
-        int split;
-        const size_t b = scratch(descs + i, count - i < kMaxDescs ? count - i : kMaxDescs, M, R,
-                                 n_adapters, n_segments, &split);
-        most = b > most ? b : most;
-    }
-    return most;
+    // launches of a call use the scratch in turn
+    return scratch(count < kMaxDescs ? count : kMaxDescs, M, R, n_adapters, n_segments, x_dtype == BC_F32);
 }
 
 bc_status bc_lora_add_batched(const bc_lora_desc *descs, int count, int64_t M, int64_t R,
@@ -613,7 +632,7 @@ bc_status bc_lora_add_batched(const bc_lora_desc *descs, int count, int64_t M, i
         return BC_ERR_UNSUPPORTED;
     if (!aligned(seg_start, 4) || !aligned(seg_adapter, 4) || !aligned(ranks, 4) || !aligned(scaling, 4))
         return BC_ERR_ALIGNMENT;
-    const size_t need = bc_workspace_size_lora(descs, count, M, R, n_adapters, n_segments);
+    const size_t need = bc_workspace_size_lora(descs, count, M, R, n_adapters, n_segments, x_dtype);
     for (int i = 0; i < count; ++i) {
         const bc_lora_desc &d = descs[i];
         if (!d.x || !d.A || !d.B || !d.y) return BC_ERR_INVALID_ARG;
@@ -643,23 +662,37 @@ bc_status bc_lora_add_batched(const bc_lora_desc *descs, int count, int64_t M, i
     a.S = (int)n_segments;
     a.R = (int)R;
     a.adapters = (int)n_adapters;
-    a.max_tiles = (int)most_tiles(M, n_segments, n_adapters);
+    a.T = tile_rows(M, n_segments, x_dtype == BC_F32);
+    a.max_tiles = (int)most_tiles(M, n_segments, n_adapters, a.T);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.head = reinterpret_cast<int *>(ws);
-    ws += round256((size_t)(1 + kGroupRows) * 4);
+    ws += round256((size_t)kGroupRows * 4);
     a.tiles = reinterpret_cast<Tile *>(ws);
-    a.v = reinterpret_cast<float *>(ws + round256((size_t)a.max_tiles * sizeof(Tile)));
+    a.v = reinterpret_cast<float4 *>(ws + round256((size_t)a.max_tiles * sizeof(Tile)));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     for (int i = 0; i < count; i += kMaxDescs) {
         a.count = count - i < kMaxDescs ? count - i : kMaxDescs;
-        scratch(descs + i, a.count, M, R, n_adapters, n_segments, &a.split);
-        const int64_t blocks = (int64_t)a.max_tiles * a.count * ((R + kChunk - 1) / kChunk);
-        a.col_blocks = 0;
+        a.col_blocks = a.chunks = 0;
+        a.steps = steps_of(descs + i, a.count, (int64_t)a.max_tiles * a.T / 16);
+        int64_t K = 0;
         for (int j = 0; j < a.count; ++j) {
             const bc_lora_desc &d = descs[i + j];
-            a.d[j] = Desc{d.x, d.A, d.B, d.y, (int)d.N, (int)d.K, split_of(d.K, blocks), a.col_blocks};
-            a.col_blocks += (int)((d.N + kCols - 1) / kCols);
+            const int blocks = (int)((d.N + kStep * a.steps - 1) / (kStep * a.steps));
+            a.d[j] = Desc{d.x, d.A, d.B, d.y, (int)d.N, (int)d.K, 0, a.col_blocks, blocks};
+            a.col_blocks += blocks;
+            K = d.K > K ? d.K : K;
         }
+        for (int j = 0, n; j < a.count; j += n) {          // neighbours that read the same x share a pass over it
+            for (n = 1; j + n < a.count && a.d[j + n].x == a.d[j].x && a.d[j + n].K == a.d[j].K;) ++n;
+            a.d[j].group_size = n;
+            a.chunks += (n * a.R + kChunk - 1) / kChunk;
+        }
+        // parts of K: enough blocks to fill the GPU about three times, with a
+        // step of 32 for every warp
+        a.split = 1;
+        while (a.split < kMaxSplit && (int64_t)a.max_tiles * a.chunks * a.split < 3 * kSms &&
+               a.split * 2 * kWarps <= (K / 32 + kWarps - 1) / kWarps * kWarps)
+            a.split *= 2;
         if (x_dtype == BC_F32)
             st = w_dtype == BC_F16 ? launch<float, __half>(a, s) : launch<float, __nv_bfloat16>(a, s);
         else
