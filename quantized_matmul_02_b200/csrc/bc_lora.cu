@@ -41,6 +41,7 @@ constexpr int kMaxSegments = 4096;
 constexpr int kMaxRank = 128;
 constexpr int kGroupRows = 256;        // up to here rows are ordered by adapter
 constexpr int kChunk = 32;             // ranks per shrink block
+constexpr int kFew = 2;                // rows up to here: plain products instead of fragments
 constexpr int kMaxSplit = 8;           // parts of K (blocks of a cluster)
 constexpr int kStep = kWarps * 32;     // columns an expand block takes at a time
 constexpr int kMaxSteps = 12;          // such steps per block
@@ -142,24 +143,32 @@ __device__ __forceinline__ void plan(const LoraArgs &a, PlanShared &p, int want,
             }
         }
         __syncthreads();
-        const int mine = p.key[tid];
+        // a row's place: how many keys come before it.  Threads lie idle where
+        // rows are few, so up to eight of them share a row.
+        const int share = M <= 32 ? 8 : M <= 64 ? 4 : M <= 128 ? 2 : 1;
+        const int who = tid / share, mine = p.key[who];
         int before = 0, same = 0, all = 0;
-        for (int j = 0; j < M; j += 4) {         // places behind M hold kNone
+        for (int j = tid % share * 4; j < M; j += share * 4) {       // places behind M hold kNone
             const int4 q = *reinterpret_cast<const int4 *>(p.key + j);
             const int k[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 before += k[e] < mine;
-                same += k[e] == mine && j + e < tid;
+                same += k[e] == mine && j + e < who;
                 all += k[e] == mine;
             }
         }
+        for (int off = 1; off < share; off <<= 1) {
+            before += __shfl_xor_sync(0xffffffffu, before, off);
+            same += __shfl_xor_sync(0xffffffffu, same, off);
+            all += __shfl_xor_sync(0xffffffffu, all, off);
+        }
         before += same;
-        const bool live = tid < M && mine != kNone, head = live && same % T == 0;
+        const bool live = tid % share == 0 && who < M && mine != kNone, head = live && same % T == 0;
         __syncthreads();
         p.key[tid] = -1;
         __syncthreads();
-        if (live) p.order[before] = tid;
+        if (live) p.order[before] = who;
         if (head) p.key[before] = tid;           // at a tile's first place: the thread that knows it
         __syncthreads();
         // place of this thread's tile among the tiles, in sorted order
@@ -247,125 +256,209 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
     const int K = a.d[first].K, blocks = a.d[first].group_size * R8;
     const int rank = a.ranks ? min(a.ranks[tile.adapter], R) : R, used = (rank + 7) / 8;
     const float scale = a.scaling ? a.scaling[tile.adapter] : 1.f;
-    const W *arow[NB];                                         // this lane's row of A, or null
     unsigned live = 0;                                         // blocks that have ranks
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        const int vb = chunk * NB + b, rb = vb % R8, r = rb * 8 + g;
-        arow[b] = nullptr;
-        if (vb < blocks && rb < used) {
-            live |= 1u << b;
-            if (r < rank)
-                arow[b] = static_cast<const W *>(a.d[first + vb / R8].A) + ((int64_t)tile.adapter * R + r) * K + t * 8;
-        }
+        const int vb = chunk * NB + b;
+        if (vb < blocks && vb % R8 < used) live |= 1u << b;
     }
-    if (!live) return;                                          // (the whole cluster)
-    const X *xrow[MB][2];
+    if (!live) return;                                         // (the whole cluster)
+    // row g of block b of A, or null
+    auto a_row = [&](int b, int g) -> const W * {
+        const int vb = chunk * NB + b, r = vb % R8 * 8 + g;
+        return (live >> b & 1) && r < rank
+                   ? static_cast<const W *>(a.d[first + vb / R8].A) + ((int64_t)tile.adapter * R + r) * K : nullptr;
+    };
+    auto x_row = [&](int i) -> const X * {
+        if (i >= n_rows) return nullptr;
+        const int64_t m = a.M <= kGroupRows ? ps.order[tile.first + i] : tile.first + i;
+        return static_cast<const X *>(a.d[first].x) + m * K;
+    };
+    constexpr int kQuads = T * kChunk / 4;
+    if (MB == 1 && n_rows <= kFew) {
+        // A row or two: plain products.  Warp w takes rank w of each block, its
+        // lanes eight neighbouring k each, 256 a step; half the instructions
+        // of the fragments, which would hold fourteen empty rows.
+        const W *ar[NB];
+        const X *xr[kFew];
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
+        for (int b = 0; b < NB; ++b) ar[b] = a_row(b, warp);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = mb * 16 + g + h * 8;
-            xrow[mb][h] = nullptr;
-            if (i < n_rows) {
-                const int64_t m = a.M <= kGroupRows ? ps.order[tile.first + i] : tile.first + i;
-                xrow[mb][h] = static_cast<const X *>(a.d[first].x) + m * K + t * 8;
+        for (int i = 0; i < kFew; ++i) xr[i] = x_row(i);
+        uint4 wa[2][NB], xa[2][kFew][kQ];
+        auto load = [&](int k, uint4 (&wa)[NB], uint4 (&xa)[kFew][kQ]) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                wa[b] = ar[b] && k < K ? *reinterpret_cast<const uint4 *>(ar[b] + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < kFew; ++i)
+#pragma unroll
+                for (int q = 0; q < kQ; ++q)
+                    xa[i][q] = xr[i] && k < K ? reinterpret_cast<const uint4 *>(xr[i] + k)[q] : make_uint4(0, 0, 0, 0);
+        };
+        float acc[kFew][NB] = {};
+        auto multiply = [&](const uint4 (&wa)[NB], const uint4 (&xa)[kFew][kQ]) {
+            float xf[kFew][8];
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) {
+                if (i >= n_rows) break;
+                const uint4 p = xa[i][0], q = xa[i][kQ - 1];
+                const uint32_t u[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (kF32) {
+                        xf[i][e] = __uint_as_float(u[e]);
+                        xf[i][e + 4] = __uint_as_float(u[e + 4]);
+                    } else {
+                        xf[i][2 * e] = __uint_as_float(u[e] << 16);
+                        xf[i][2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+                    }
+                }
             }
-        }
-    auto load = [&](int u, uint4 (&wa)[NB], uint4 (&xa)[MB][2][kQ]) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-            wa[b] = arow[b] ? *reinterpret_cast<const uint4 *>(arow[b] + u * 32) : make_uint4(0, 0, 0, 0);
+            for (int b = 0; b < NB; ++b) {
+                if (!(live >> b & 1)) continue;
+                const uint32_t u[4] = {wa[b].x, wa[b].y, wa[b].z, wa[b].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t w0, w1;
+                    widen<W>(u[e], w0, w1);
+#pragma unroll
+                    for (int i = 0; i < kFew; ++i)
+                        if (i < n_rows)
+                            acc[i][b] = fmaf(xf[i][2 * e + 1], __uint_as_float(w1),
+                                             fmaf(xf[i][2 * e], __uint_as_float(w0), acc[i][b]));
+                }
+            }
+        };
+        const int step = a.split * 256;
+        int k = part * 256 + lane * 8;
+        load(k, wa[0], xa[0]);
+        for (int k0 = part * 256; k0 < K; k0 += 2 * step, k += 2 * step) {
+            load(k + step, wa[1], xa[1]);
+            multiply(wa[0], xa[0]);
+            load(k + 2 * step, wa[0], xa[0]);
+            multiply(wa[1], xa[1]);
+        }
+#pragma unroll
+        for (int i = 0; i < kFew; ++i)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float s = acc[i][b];
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+                // its place among the fragments; rows that the tile lacks stay unset: no one reads them
+                if (lane == 0) reinterpret_cast<float *>(red)[(b * 32 + i * 4 + warp / 2) * 4 + (warp & 1)] = s;
+            }
+    } else {
+        const W *arow[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            arow[b] = a_row(b, g);
+            if (arow[b]) arow[b] += t * 8;
+        }
+        const X *xrow[MB][2];
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int q = 0; q < kQ; ++q)
-                    xa[mb][h][q] = xrow[mb][h] ? reinterpret_cast<const uint4 *>(xrow[mb][h] + u * 32)[q]
-                                               : make_uint4(0, 0, 0, 0);
-    };
-    float acc[MB][NB][4] = {};
-    auto multiply = [&](const uint4 (&wa)[NB], const uint4 (&xa)[MB][2][kQ]) {
-        if constexpr (kBf16) {
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb) {
-                if (mb * 16 >= n_rows) break;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint4 &p = xa[mb][0][0], &q = xa[mb][1][0];
-                    const uint32_t f[4] = {s ? p.z : p.x, s ? q.z : q.x, s ? p.w : p.y, s ? q.w : q.y};
-#pragma unroll
-                    for (int b = 0; b < kChunk / 8; ++b)
-                        if (live >> b & 1) mma_bf16(acc[mb][b], f, s ? wa[b].z : wa[b].x, s ? wa[b].w : wa[b].y);
-                }
+            for (int h = 0; h < 2; ++h) {
+                xrow[mb][h] = x_row(mb * 16 + g + h * 8);
+                if (xrow[mb][h]) xrow[mb][h] += t * 8;
             }
-        } else {
+        auto load = [&](int u, uint4 (&wa)[NB], uint4 (&xa)[MB][2][kQ]) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {              // two of the lane's eight k each
-                uint32_t w0[kChunk / 8], w1[kChunk / 8];
+            for (int b = 0; b < NB; ++b)
+                wa[b] = arow[b] ? *reinterpret_cast<const uint4 *>(arow[b] + u * 32) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int b = 0; b < kChunk / 8; ++b)
-                    widen<W>(s == 0 ? wa[b].x : s == 1 ? wa[b].y : s == 2 ? wa[b].z : wa[b].w, w0[b], w1[b]);
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < kQ; ++q)
+                        xa[mb][h][q] = xrow[mb][h] ? reinterpret_cast<const uint4 *>(xrow[mb][h] + u * 32)[q]
+                                                   : make_uint4(0, 0, 0, 0);
+        };
+        float acc[MB][NB][4] = {};
+        auto multiply = [&](const uint4 (&wa)[NB], const uint4 (&xa)[MB][2][kQ]) {
+            if constexpr (kBf16) {
 #pragma unroll
                 for (int mb = 0; mb < MB; ++mb) {
                     if (mb * 16 >= n_rows) break;
-                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if constexpr (kF32) {
-                            const uint4 &p = xa[mb][h][s >> 1];
-                            split_tf32(__uint_as_float(s & 1 ? p.z : p.x), hi[h], lo[h]);
-                            split_tf32(__uint_as_float(s & 1 ? p.w : p.y), hi[h + 2], lo[h + 2]);
-                        } else {
-                            const uint4 &p = xa[mb][h][0];
-                            widen<__nv_bfloat16>(s == 0 ? p.x : s == 1 ? p.y : s == 2 ? p.z : p.w, hi[h], hi[h + 2]);
-                        }
+                    for (int s = 0; s < 2; ++s) {
+                        const uint4 &p = xa[mb][0][0], &q = xa[mb][1][0];
+                        const uint32_t f[4] = {s ? p.z : p.x, s ? q.z : q.x, s ? p.w : p.y, s ? q.w : q.y};
+#pragma unroll
+                        for (int b = 0; b < kChunk / 8; ++b)
+                            if (live >> b & 1) mma_bf16(acc[mb][b], f, s ? wa[b].z : wa[b].x, s ? wa[b].w : wa[b].y);
                     }
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {              // two of the lane's eight k each
+                    uint32_t w0[kChunk / 8], w1[kChunk / 8];
 #pragma unroll
                     for (int b = 0; b < kChunk / 8; ++b)
-                        if (live >> b & 1) {
-                            if constexpr (kF32)
-                                mma_tf32(acc[mb][b], lo[0], lo[1], lo[2], lo[3], w0[b], w1[b]);
-                            mma_tf32(acc[mb][b], hi[0], hi[1], hi[2], hi[3], w0[b], w1[b]);
+                        widen<W>(s == 0 ? wa[b].x : s == 1 ? wa[b].y : s == 2 ? wa[b].z : wa[b].w, w0[b], w1[b]);
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb) {
+                        if (mb * 16 >= n_rows) break;
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if constexpr (kF32) {
+                                const uint4 &p = xa[mb][h][s >> 1];
+                                split_tf32(__uint_as_float(s & 1 ? p.z : p.x), hi[h], lo[h]);
+                                split_tf32(__uint_as_float(s & 1 ? p.w : p.y), hi[h + 2], lo[h + 2]);
+                            } else {
+                                const uint4 &p = xa[mb][h][0];
+                                widen<__nv_bfloat16>(s == 0 ? p.x : s == 1 ? p.y : s == 2 ? p.z : p.w, hi[h], hi[h + 2]);
+                            }
                         }
+#pragma unroll
+                        for (int b = 0; b < kChunk / 8; ++b)
+                            if (live >> b & 1) {
+                                if constexpr (kF32)
+                                    mma_tf32(acc[mb][b], lo[0], lo[1], lo[2], lo[3], w0[b], w1[b]);
+                                mma_tf32(acc[mb][b], hi[0], hi[1], hi[2], hi[3], w0[b], w1[b]);
+                            }
+                    }
                 }
             }
+        };
+        // the next step's pieces are on their way while this one's are multiplied
+        uint4 wa[2][NB], xa[2][MB][2][kQ];
+        const int step = a.split * kWarps, units = K / 32;
+        int u = part * kWarps + warp;
+        if (u < units) load(u, wa[0], xa[0]);
+        for (; u < units; u += 2 * step) {
+            if (u + step < units) load(u + step, wa[1], xa[1]);
+            multiply(wa[0], xa[0]);
+            if (u + step < units) {
+                if (u + 2 * step < units) load(u + 2 * step, wa[0], xa[0]);
+                multiply(wa[1], xa[1]);
+            }
         }
-    };
-    // the next step's pieces are on their way while this one's are multiplied
-    uint4 wa[2][NB], xa[2][MB][2][kQ];
-    const int step = a.split * kWarps, units = K / 32;
-    int u = part * kWarps + warp;
-    if (u < units) load(u, wa[0], xa[0]);
-    for (; u < units; u += 2 * step) {
-        if (u + step < units) load(u + step, wa[1], xa[1]);
-        multiply(wa[0], xa[0]);
-        if (u + step < units) {
-            if (u + 2 * step < units) load(u + 2 * step, wa[0], xa[0]);
-            multiply(wa[1], xa[1]);
+        // the block's sum over its warps, in fragment order
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                red[warp * kQuads + (mb * NB + b) * 32 + lane] =
+                    make_float4(acc[mb][b][0], acc[mb][b][1], acc[mb][b][2], acc[mb][b][3]);
+        __syncthreads();
+        for (int i = tid; i < kQuads; i += kThreads) {
+            float4 s = red[i];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) {
+                const float4 p = red[w * kQuads + i];
+                s.x += p.x;
+                s.y += p.y;
+                s.z += p.z;
+                s.w += p.w;
+            }
+            red[i] = s;
         }
-    }
-    // the block's sum over its warps, in fragment order
-    constexpr int kQuads = T * kChunk / 4;
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-            red[warp * kQuads + (mb * NB + b) * 32 + lane] =
-                make_float4(acc[mb][b][0], acc[mb][b][1], acc[mb][b][2], acc[mb][b][3]);
-    __syncthreads();
-    for (int i = tid; i < kQuads; i += kThreads) {
-        float4 s = red[i];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            const float4 p = red[w * kQuads + i];
-            s.x += p.x;
-            s.y += p.y;
-            s.z += p.z;
-            s.w += p.w;
-        }
-        red[i] = s;
     }
     // the cluster's sum: every block takes a share of the places
     cg::cluster_group cluster = cg::this_cluster();
