@@ -108,9 +108,9 @@ def _load() -> ctypes.CDLL:
     lib.bc_add_rmsnorm_q8.argtypes = [P, i32, P, i32, P, i32, i64, i64, f32, P, P, P, P]
     lib.bc_lora_add.argtypes = [P, i32, P, P, i32, i64, i64, i64, i64, i64, P, P, i64, P, P,
                                 P, P, sz, P]
-    lib.bc_lora_add_batched.argtypes = [ctypes.POINTER(LoraDesc), i32, i64, i64, i64, i32, i32,
+    lib.bc_lora_add_batched.argtypes = [P, i32, i64, i64, i64, i32, i32,
                                         P, P, i64, P, P, P, sz, P]
-    lib.bc_workspace_size_lora.argtypes = [ctypes.POINTER(LoraDesc), i32, i64, i64, i64, i64, i32]
+    lib.bc_workspace_size_lora.argtypes = [P, i32, i64, i64, i64, i64, i32]
     lib.bc_workspace_size_lora.restype = sz
     lib.bc_beam_select.argtypes = [P, P, P, i64, i64, i64, i64, i32, i32, P, P, P, P, P, sz, P]
     lib.bc_workspace_size_beam.argtypes = [i64, i64, i64, i64]
@@ -119,7 +119,7 @@ def _load() -> ctypes.CDLL:
                                      i64, i32, i32, P, P, P, P, P, sz, P]
     lib.bc_workspace_size_matmul_beam.argtypes = [i64, i64, i64, i64, i64, i32, i32]
     lib.bc_workspace_size_matmul_beam.restype = sz
-    lib.bc_beam_reorder.argtypes = [ctypes.POINTER(BeamState), i32, P, i64, i64, i64, P]
+    lib.bc_beam_reorder.argtypes = [P, i32, P, i64, i64, i64, P]
     for name in ("bc_add_rmsnorm", "bc_add_rmsnorm_q8", "bc_lora_add", "bc_lora_add_batched",
                  "bc_beam_select", "bc_matmul_q_beam", "bc_beam_reorder"):
         getattr(lib, name).restype = i32
@@ -349,69 +349,66 @@ def matmul_q_argmax(x: torch.Tensor, W: torch.Tensor, scales: Optional[torch.Ten
 # ---------------------------------------------------------------------------
 # Around the projections: norm, adapters, beam search.  These calls take
 # tensors of one device, run there (also when it is not the current one), and
-# check shapes and types before the C call sees pointers.
+# check shapes and types before the C call sees pointers.  A decode step makes
+# hundreds of them, so the checks are kept to a few attribute reads a tensor.
 # ---------------------------------------------------------------------------
-def _one_device(what: str, *tensors: Optional[torch.Tensor]) -> torch.device:
-    dev = None
+_F32, _F16, _BF16 = torch.float32, torch.float16, torch.bfloat16
+_I32, _U8 = torch.int32, torch.uint8
+_FLOATS = (_F32, _F16, _BF16)
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _one_device(what: str, first: torch.Tensor, *tensors: Optional[torch.Tensor]) -> int:
+    """Index of the device that holds all of them, contiguous."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"{what}: expected CUDA tensors")
+    if not first.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous tensors")
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{what}: expected CUDA tensors")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: expected contiguous tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{what}: all tensors must be on one device")
+        if t is not None:
+            if t.get_device() != dev:
+                raise ValueError(f"{what}: all tensors must be on one CUDA device")
+            if not t.is_contiguous():
+                raise ValueError(f"{what}: expected contiguous tensors")
     return dev
 
 
-def _want(what: str, name: str, t: Optional[torch.Tensor], shape, *dtypes) -> None:
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype not in dtypes):
-        raise ValueError(f"{what}: {name} must be {' or '.join(map(str, dtypes))} {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
+def _bad(what: str, name: str, t: torch.Tensor, shape, *dtypes) -> None:
+    raise ValueError(f"{what}: {name} must be {' or '.join(map(str, dtypes))} {tuple(shape)}, "
+                     f"got {t.dtype} {tuple(t.shape)}")
 
 
-class _Launch:
-    """The device and stream of one call: `with` makes both current, so that
-    outputs and scratch made inside belong to that stream."""
-    __slots__ = ("dev", "stream", "prev_dev", "ctx")
+def _want(what: str, name: str, t: torch.Tensor, shape: tuple, *dtypes) -> None:
+    if t.dtype not in dtypes or t.shape != shape:
+        _bad(what, name, t, shape, *dtypes)
 
-    def __init__(self, what: str, dev: torch.device, stream: Optional[torch.cuda.Stream]):
-        if stream is not None and stream.device != dev:
+
+def _elsewhere(what: str, dev: int, stream: Optional[torch.cuda.Stream]):
+    """None when the call runs on the current device's current stream; else
+    the context that makes its device and stream current, so that outputs and
+    scratch made inside belong to that stream."""
+    if stream is not None:
+        if stream.device.index != dev:
             raise ValueError(f"{what}: the stream belongs to another device than the tensors")
-        self.dev, self.stream, self.ctx = dev, stream, None
-
-    def __enter__(self) -> int:
-        if self.stream is not None:
-            self.ctx = torch.cuda.stream(self.stream)
-        elif self.dev.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(self.dev)
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        return torch.cuda.stream(stream)
+    return None if dev == _current_device() else torch.cuda.device(dev)
 
 
 def _p(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
-
-
-def _norm_args(what, x, weight, eps, residual):
-    if x.dim() < 1 or x.dtype not in _FLOATS or x.numel() == 0:
+def _norm_args(what, x, weight, residual):
+    if x.dtype not in _FLOATS or x.dim() < 1 or x.numel() == 0:
         raise ValueError(f"{what}: x must be a float tensor [..., D] with elements")
-    D = x.shape[-1]
-    if weight is not None:
-        _want(what, "weight", weight, (D,), *_FLOATS)
-    if residual is not None:
-        _want(what, "residual", residual, x.shape, *_FLOATS)
+    shape = x.shape
+    D = shape[-1]
+    if weight is not None and (weight.dtype not in _FLOATS or weight.shape != (D,)):
+        _bad(what, "weight", weight, (D,), *_FLOATS)
+    if residual is not None and (residual.dtype not in _FLOATS or residual.shape != shape):
+        _bad(what, "residual", residual, shape, *_FLOATS)
     return x.numel() // D, D
 
 
@@ -421,21 +418,23 @@ def add_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e
     """h = x + residual; residual <- h; returns h / rms(h) * weight over the
     last dimension, in `out_dtype` (default: x's).  `residual` is updated in
     place; `out` may be x."""
-    M, D = _norm_args("add_rmsnorm", x, weight, eps, residual)
+    what = "add_rmsnorm"
+    M, D = _norm_args(what, x, weight, residual)
     if out is not None:
-        out_dtype = out.dtype
-        _want("add_rmsnorm", "out", out, x.shape, *_FLOATS)
-    elif out_dtype is None:
-        out_dtype = x.dtype
-    elif out_dtype not in _FLOATS:
-        raise ValueError("add_rmsnorm: out_dtype must be float32, float16 or bfloat16")
-    with _Launch("add_rmsnorm", _one_device("add_rmsnorm", x, weight, residual, out), stream) as s:
-        if out is None:
-            out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
-        _check(lib.bc_add_rmsnorm(x.data_ptr(), _DT[x.dtype], _p(residual),
-                                  _DT[residual.dtype] if residual is not None else BC_F32,
-                                  _p(weight), _DT[weight.dtype] if weight is not None else BC_F32,
-                                  M, D, eps, out.data_ptr(), _DT[out_dtype], s), "bc_add_rmsnorm")
+        _want(what, "out", out, x.shape, *_FLOATS)
+    elif out_dtype is not None and out_dtype not in _FLOATS:
+        raise ValueError(f"{what}: out_dtype must be float32, float16 or bfloat16")
+    dev = _one_device(what, x, weight, residual, out)
+    other = _elsewhere(what, dev, stream)
+    if other is not None:
+        with other:
+            return add_rmsnorm(x, weight, eps, residual, out, out_dtype)
+    if out is None:
+        out = torch.empty_like(x, dtype=out_dtype)
+    _check(lib.bc_add_rmsnorm(x.data_ptr(), _DT[x.dtype], _p(residual),
+                              BC_F32 if residual is None else _DT[residual.dtype], _p(weight),
+                              BC_F32 if weight is None else _DT[weight.dtype], M, D, eps,
+                              out.data_ptr(), _DT[out.dtype], _raw_stream(dev)), "bc_add_rmsnorm")
     return out
 
 
@@ -446,68 +445,79 @@ def add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float =
     """add_rmsnorm with the output as (codes uint8 [..., D], scales, zeros fp16
     [..., D/64]): what matmul_q reads as packed weights of 8 bits."""
     what = "add_rmsnorm_q8"
-    M, D = _norm_args(what, x, weight, eps, residual)
+    M, D = _norm_args(what, x, weight, residual)
     if D % 64:
         raise ValueError(f"{what}: D must be a multiple of 64")
     gs = (*x.shape[:-1], D // 64)
     if codes is not None:
-        _want(what, "codes", codes, x.shape, torch.uint8)
+        _want(what, "codes", codes, x.shape, _U8)
     if scales is not None:
-        _want(what, "scales", scales, gs, torch.float16)
+        _want(what, "scales", scales, gs, _F16)
     if zeros is not None:
-        _want(what, "zeros", zeros, gs, torch.float16)
-    with _Launch(what, _one_device(what, x, weight, residual, codes, scales, zeros), stream) as s:
-        if codes is None:
-            codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-        if scales is None:
-            scales = torch.empty(gs, dtype=torch.float16, device=x.device)
-        if zeros is None:
-            zeros = torch.empty(gs, dtype=torch.float16, device=x.device)
-        _check(lib.bc_add_rmsnorm_q8(x.data_ptr(), _DT[x.dtype], _p(residual),
-                                     _DT[residual.dtype] if residual is not None else BC_F32,
-                                     _p(weight), _DT[weight.dtype] if weight is not None else BC_F32,
-                                     M, D, eps, codes.data_ptr(), scales.data_ptr(),
-                                     zeros.data_ptr(), s), "bc_add_rmsnorm_q8")
+        _want(what, "zeros", zeros, gs, _F16)
+    dev = _one_device(what, x, weight, residual, codes, scales, zeros)
+    other = _elsewhere(what, dev, stream)
+    if other is not None:
+        with other:
+            return add_rmsnorm_q8(x, weight, eps, residual, codes, scales, zeros)
+    if codes is None:
+        codes = torch.empty_like(x, dtype=_U8)
+    if scales is None:
+        scales = torch.empty(gs, dtype=_F16, device=x.device)
+    if zeros is None:
+        zeros = torch.empty(gs, dtype=_F16, device=x.device)
+    _check(lib.bc_add_rmsnorm_q8(x.data_ptr(), _DT[x.dtype], _p(residual),
+                                 BC_F32 if residual is None else _DT[residual.dtype], _p(weight),
+                                 BC_F32 if weight is None else _DT[weight.dtype], M, D, eps,
+                                 codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
+                                 _raw_stream(dev)), "bc_add_rmsnorm_q8")
     return codes, scales, zeros
 
 
 class LoraDescs:
     """The projections of one lora_add_batched call (from make_lora_descs);
-    holds its tensors.  Keep it for the steps that use the same buffers."""
-    __slots__ = ("array", "M", "R", "n_adapters", "x_dtype", "w_dtype", "device", "tensors")
+    holds their tensors.  Keep it for the steps that use the same buffers."""
+    __slots__ = ("array", "count", "M", "R", "n_adapters", "x_dtype", "w_dtype", "device", "tensors")
 
 
 def make_lora_descs(items: Sequence[tuple]) -> LoraDescs:
     """items: (x, A, B, y) per projection: x [M][K] fp32 or bf16, A
-    [n_adapters][R][K] and B [n_adapters][N][R] fp16 or bf16, y fp32 [M][N]."""
+    [n_adapters][R][K] and B [n_adapters][N][R] fp16 or bf16, y fp32 [M][N].
+    Neighbours that read the same x share a pass over it."""
     what = "make_lora_descs"
     if not items:
         raise ValueError(f"{what}: no projections")
     x0, A0 = items[0][0], items[0][1]
+    xt, wt = x0.dtype, A0.dtype
     if x0.dim() != 2 or A0.dim() != 3:
         raise ValueError(f"{what}: x must be [M][K] and A [n_adapters][R][K]")
-    if x0.dtype not in (torch.float32, torch.bfloat16) or A0.dtype not in (torch.float16, torch.bfloat16):
+    if xt not in (_F32, _BF16) or wt not in (_F16, _BF16):
         raise ValueError(f"{what}: x must be float32 or bfloat16, adapters float16 or bfloat16")
+    M, (n, R, _) = x0.shape[0], A0.shape
+    dev = x0.get_device()
+    fields = []
+    for x, A, B, y in items:
+        _one_device(what, x0, x, A, B, y)
+        K, N = x.shape[-1], y.shape[-1]
+        if x.dtype != xt or x.shape != (M, K):
+            _bad(what, "x", x, (M, K), xt)
+        if A.dtype != wt or A.shape != (n, R, K):
+            _bad(what, "A", A, (n, R, K), wt)
+        if B.dtype != wt or B.shape != (n, N, R):
+            _bad(what, "B", B, (n, N, R), wt)
+        if y.dtype != _F32 or y.shape != (M, N):
+            _bad(what, "y", y, (M, N), _F32)
+        fields += (x.data_ptr(), A.data_ptr(), B.data_ptr(), y.data_ptr(), N, K)
     d = LoraDescs()
-    d.M, (d.n_adapters, d.R) = x0.shape[0], A0.shape[:2]
-    d.x_dtype, d.w_dtype, d.tensors = _DT[x0.dtype], _DT[A0.dtype], list(items)
-    d.array = (LoraDesc * len(items))()
-    d.device = _one_device(what, *(t for item in items for t in item))
-    for i, (x, A, B, y) in enumerate(items):
-        if x.dim() != 2 or y.dim() != 2:
-            raise ValueError(f"{what}: x must be [M][K] and y [M][N]")
-        K, N = x.shape[1], y.shape[1]
-        _want(what, "x", x, (d.M, K), x0.dtype)
-        _want(what, "A", A, (d.n_adapters, d.R, K), A0.dtype)
-        _want(what, "B", B, (d.n_adapters, N, d.R), A0.dtype)
-        _want(what, "y", y, (d.M, N), torch.float32)
-        d.array[i] = LoraDesc(x.data_ptr(), A.data_ptr(), B.data_ptr(), y.data_ptr(), N, K)
+    d.M, d.n_adapters, d.R, d.count, d.device = M, n, R, len(items), dev
+    d.x_dtype, d.w_dtype, d.tensors = _DT[xt], _DT[wt], items
+    d.array = (ctypes.c_int64 * len(fields))(*fields)       # bc_lora_desc: six 8-byte fields
     return d
 
 
 def workspace_size_lora(descs: LoraDescs, n_segments: int) -> int:
-    return int(lib.bc_workspace_size_lora(descs.array, len(descs.array), descs.M, descs.R,
-                                          descs.n_adapters, n_segments, descs.x_dtype))
+    return lib.bc_workspace_size_lora(descs.array, descs.count, descs.M, descs.R,
+                                      descs.n_adapters, n_segments, descs.x_dtype)
 
 
 def lora_add_batched(descs: LoraDescs, seg_start: torch.Tensor, seg_adapter: torch.Tensor,
@@ -519,25 +529,28 @@ def lora_add_batched(descs: LoraDescs, seg_start: torch.Tensor, seg_adapter: tor
     (outside 0..n_adapters-1: none).  seg_start int32 [S+1], seg_adapter int32
     [S]; ranks int32 and scaling fp32 [n_adapters], or None."""
     what = "lora_add_batched"
-    S = seg_adapter.numel()
-    _want(what, "seg_adapter", seg_adapter, (S,), torch.int32)
-    _want(what, "seg_start", seg_start, (S + 1,), torch.int32)
-    if ranks is not None:
-        _want(what, "ranks", ranks, (descs.n_adapters,), torch.int32)
-    if scaling is not None:
-        _want(what, "scaling", scaling, (descs.n_adapters,), torch.float32)
+    S, n = seg_adapter.numel(), descs.n_adapters
+    if seg_adapter.dtype != _I32 or seg_adapter.dim() != 1:
+        _bad(what, "seg_adapter", seg_adapter, (S,), _I32)
+    if seg_start.dtype != _I32 or seg_start.shape != (S + 1,):
+        _bad(what, "seg_start", seg_start, (S + 1,), _I32)
+    if ranks is not None and (ranks.dtype != _I32 or ranks.shape != (n,)):
+        _bad(what, "ranks", ranks, (n,), _I32)
+    if scaling is not None and (scaling.dtype != _F32 or scaling.shape != (n,)):
+        _bad(what, "scaling", scaling, (n,), _F32)
     dev = _one_device(what, seg_start, seg_adapter, ranks, scaling, workspace)
     if dev != descs.device:
-        raise ValueError(f"{what}: all tensors must be on one device")
-    with _Launch(what, dev, stream) as s:
-        if workspace is None:
-            workspace = torch.empty(workspace_size_lora(descs, S), dtype=torch.uint8, device=dev)
-        _check(lib.bc_lora_add_batched(descs.array, len(descs.array), descs.M, descs.R,
-                                       descs.n_adapters, descs.x_dtype, descs.w_dtype,
-                                       seg_start.data_ptr(), seg_adapter.data_ptr(), S,
-                                       _p(ranks), _p(scaling), workspace.data_ptr(),
-                                       workspace.numel() * workspace.element_size(), s),
-               "bc_lora_add_batched")
+        raise ValueError(f"{what}: all tensors must be on one CUDA device")
+    other = _elsewhere(what, dev, stream)
+    if other is not None:
+        with other:
+            return lora_add_batched(descs, seg_start, seg_adapter, ranks, scaling, workspace)
+    if workspace is None:
+        workspace = torch.empty(workspace_size_lora(descs, S), dtype=_U8, device=seg_start.device)
+    _check(lib.bc_lora_add_batched(descs.array, descs.count, descs.M, descs.R, n, descs.x_dtype,
+                                   descs.w_dtype, seg_start.data_ptr(), seg_adapter.data_ptr(), S,
+                                   _p(ranks), _p(scaling), workspace.data_ptr(), workspace.nbytes,
+                                   _raw_stream(dev)), "bc_lora_add_batched")
 
 
 def lora_add(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, y: torch.Tensor,
@@ -551,18 +564,17 @@ def lora_add(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, y: torch.Tensor,
 
 
 def workspace_size_beam(batch: int, beams: int, V: int, n_out: int) -> int:
-    return int(lib.bc_workspace_size_beam(batch, beams, V, n_out))
+    return lib.bc_workspace_size_beam(batch, beams, V, n_out)
 
 
-def _beam_out(what, dev, batch, n_out, out):
+def _beam_out(what, device, batch, n_out, out):
+    shape = (batch, n_out)
     if out is None:
-        return (torch.empty((batch, n_out), dtype=torch.float32, device=dev),
-                torch.empty((batch, n_out), dtype=torch.int32, device=dev),
-                torch.empty((batch, n_out), dtype=torch.int32, device=dev),
-                torch.empty((batch, n_out), dtype=torch.uint8, device=dev))
+        return (torch.empty(shape, dtype=_F32, device=device), torch.empty(shape, dtype=_I32, device=device),
+                torch.empty(shape, dtype=_I32, device=device), torch.empty(shape, dtype=_U8, device=device))
     for t, name, dt in zip(out, ("out scores", "parent", "token", "out finished"),
-                           (torch.float32, torch.int32, torch.int32, torch.uint8)):
-        _want(what, name, t, (batch, n_out), dt)
+                           (_F32, _I32, _I32, _U8)):
+        _want(what, name, t, shape, dt)
     return tuple(out)
 
 
@@ -579,27 +591,29 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int,
         raise ValueError(f"{what}: logits must be [batch * beams][V], scores [batch][beams]")
     batch, beams = scores.shape
     V = logits.shape[1]
-    _want(what, "logits", logits, (batch * beams, V), torch.float32)
-    _want(what, "scores", scores, (batch, beams), torch.float32)
+    _want(what, "logits", logits, (batch * beams, V), _F32)
+    _want(what, "scores", scores, (batch, beams), _F32)
     if finished is not None:
-        _want(what, "finished", finished, (batch, beams), torch.uint8, torch.bool)
+        _want(what, "finished", finished, (batch, beams), _U8, torch.bool)
     dev = _one_device(what, logits, scores, finished, workspace, *(out or ()))
-    with _Launch(what, dev, stream) as s:
-        o = _beam_out(what, dev, batch, n_out, out)
-        need = workspace_size_beam(batch, beams, V, n_out)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        _check(lib.bc_beam_select(logits.data_ptr(), scores.data_ptr(), _p(finished), batch, beams,
-                                  V, n_out, eos, pad, o[0].data_ptr(), o[1].data_ptr(),
-                                  o[2].data_ptr(), o[3].data_ptr(), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), s),
-               "bc_beam_select")
+    other = _elsewhere(what, dev, stream)
+    if other is not None:
+        with other:
+            return beam_select(logits, scores, n_out, finished, eos, pad, out, workspace)
+    o = _beam_out(what, logits.device, batch, n_out, out)
+    if workspace is None:
+        workspace = torch.empty(lib.bc_workspace_size_beam(batch, beams, V, n_out), dtype=_U8,
+                                device=logits.device)
+    _check(lib.bc_beam_select(logits.data_ptr(), scores.data_ptr(), _p(finished), batch, beams, V,
+                              n_out, eos, pad, o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr(),
+                              o[3].data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                              _raw_stream(dev)), "bc_beam_select")
     return o
 
 
 def workspace_size_matmul_beam(batch: int, beams: int, N: int, K: int, n_out: int, mode: int,
                                x_dtype: int = BC_F32) -> int:
-    return int(lib.bc_workspace_size_matmul_beam(batch, beams, N, K, n_out, mode, x_dtype))
+    return lib.bc_workspace_size_matmul_beam(batch, beams, N, K, n_out, mode, x_dtype)
 
 
 def matmul_q_beam(x: torch.Tensor, W: torch.Tensor, scales: Optional[torch.Tensor],
@@ -613,42 +627,44 @@ def matmul_q_beam(x: torch.Tensor, W: torch.Tensor, scales: Optional[torch.Tenso
     what = "matmul_q_beam"
     if beam_scores.dim() != 2 or x.dim() != 2 or x.shape[0] != beam_scores.numel():
         raise ValueError(f"{what}: x must be [batch * beams][K], beam_scores [batch][beams]")
-    if x.dtype not in (torch.float32, torch.bfloat16):
+    if x.dtype not in (_F32, _BF16):
         raise ValueError(f"{what}: x must be float32 or bfloat16")
     batch, beams = beam_scores.shape
     K, N = x.shape[1], W.shape[0]
     packed = mode == BC_MODE_PACKED
-    if packed:
-        _want(what, "W", W, (N, K * bits // 8), torch.uint8)
-    else:
-        _want(what, "W", W, (N, K), torch.float16)
+    _want(what, "W", W, (N, K * bits // 8) if packed else (N, K), _U8 if packed else _F16)
     if packed or bits != 16:
         groups = K // 64 if group == 64 else 1
-        sz = torch.float16 if packed else torch.int32 if mode == BC_MODE_RUNTIME_RANGE else torch.float32
+        sz = _F16 if packed else _I32 if mode == BC_MODE_RUNTIME_RANGE else _F32
+        if scales is None or (zeros is None and mode != BC_MODE_RUNTIME_RANGE):
+            raise ValueError(f"{what}: this mode needs scales and zeros")
         _want(what, "scales", scales, (N, groups), sz)
         if mode != BC_MODE_RUNTIME_RANGE:
             _want(what, "zeros", zeros, (N, groups), sz)
-    _want(what, "beam_scores", beam_scores, (batch, beams), torch.float32)
+    _want(what, "beam_scores", beam_scores, (batch, beams), _F32)
     if finished is not None:
-        _want(what, "finished", finished, (batch, beams), torch.uint8, torch.bool)
+        _want(what, "finished", finished, (batch, beams), _U8, torch.bool)
     dev = _one_device(what, x, W, scales, zeros, beam_scores, finished, workspace, *(out or ()))
-    with _Launch(what, dev, stream) as s:
-        o = _beam_out(what, dev, batch, n_out, out)
+    other = _elsewhere(what, dev, stream)
+    if other is not None:
+        with other:
+            return matmul_q_beam(x, W, scales, zeros, bits, group, mode, beam_scores, n_out,
+                                 finished, eos, pad, out, workspace)
+    o = _beam_out(what, x.device, batch, n_out, out)
+    if workspace is None:
         need = workspace_size_matmul_beam(batch, beams, N, K, n_out, mode, _DT[x.dtype])
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        _check(lib.bc_matmul_q_beam(x.data_ptr(), _DT[x.dtype], W.data_ptr(), _p(scales), _p(zeros),
-                                    batch, beams, N, K, bits, group, mode, beam_scores.data_ptr(),
-                                    _p(finished), n_out, eos, pad, o[0].data_ptr(), o[1].data_ptr(),
-                                    o[2].data_ptr(), o[3].data_ptr(), workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), s),
-               "bc_matmul_q_beam")
+        workspace = torch.empty(need, dtype=_U8, device=x.device)
+    _check(lib.bc_matmul_q_beam(x.data_ptr(), _DT[x.dtype], W.data_ptr(), _p(scales), _p(zeros),
+                                batch, beams, N, K, bits, group, mode, beam_scores.data_ptr(),
+                                _p(finished), n_out, eos, pad, o[0].data_ptr(), o[1].data_ptr(),
+                                o[2].data_ptr(), o[3].data_ptr(), workspace.data_ptr(),
+                                workspace.nbytes, _raw_stream(dev)), "bc_matmul_q_beam")
     return o
 
 
 class BeamStates:
-    """States of beam_reorder (from make_beam_states); holds its tensors."""
-    __slots__ = ("array", "beams_total", "device", "tensors")
+    """States of beam_reorder (from make_beam_states); holds their tensors."""
+    __slots__ = ("array", "count", "beams_total", "device", "tensors")
 
 
 def make_beam_states(tensors: Sequence[torch.Tensor]) -> BeamStates:
@@ -659,17 +675,19 @@ def make_beam_states(tensors: Sequence[torch.Tensor]) -> BeamStates:
     what = "make_beam_states"
     if not tensors:
         raise ValueError(f"{what}: no states")
-    st = BeamStates()
-    st.beams_total, st.device, st.tensors = tensors[0].shape[0], tensors[0].device, list(tensors)
-    st.array = (BeamState * len(tensors))()
+    dev, total = tensors[0].get_device(), tensors[0].shape[0]
+    if dev < 0:
+        raise ValueError(f"{what}: expected CUDA tensors")
+    fields = []
     for i, t in enumerate(tensors):
-        if not t.is_cuda or t.device != st.device:
+        shape, strides, size = t.shape, t.stride(), t.element_size()
+        if t.get_device() != dev:
             raise ValueError(f"{what}: all states must be on one CUDA device")
-        shape, strides = t.shape, t.stride()
-        if shape[0] != st.beams_total or t.numel() == 0:
+        if shape[0] != total or t.numel() == 0:
             raise ValueError(f"{what}: every state must be [batch * beams, ...] with elements")
-        run, rows, row_stride, size = 1, 1, 0, t.element_size()
-        for n, s in zip(reversed(shape[1:]), reversed(strides[1:])):
+        run, rows, row_stride = 1, 1, 0
+        for k in range(len(shape) - 1, 0, -1):
+            n, s = shape[k], strides[k]
             if n == 1:
                 continue
             if rows == 1 and s == run:
@@ -682,8 +700,11 @@ def make_beam_states(tensors: Sequence[torch.Tensor]) -> BeamStates:
                 raise ValueError(f"{what}: state {i} is not runs of contiguous elements at one stride")
         if rows > 1 and row_stride < run:
             raise ValueError(f"{what}: state {i} overlaps itself")
-        beam = strides[0] if shape[0] > 1 else max(strides[0], run)
-        st.array[i] = BeamState(t.data_ptr(), rows, run * size, row_stride * size, beam * size)
+        beam = strides[0] if total > 1 else max(strides[0], run)
+        fields += (t.data_ptr(), rows, run * size, row_stride * size, beam * size)
+    st = BeamStates()
+    st.beams_total, st.device, st.tensors, st.count = total, dev, tensors, len(tensors)
+    st.array = (ctypes.c_int64 * len(fields))(*fields)      # bc_beam_state: five 8-byte fields
     return st
 
 
@@ -694,14 +715,18 @@ def beam_reorder(states, parent: torch.Tensor, stream=None) -> None:
     what = "beam_reorder"
     if not isinstance(states, BeamStates):
         states = make_beam_states(states)
-    if parent.dim() != 2 or parent.dtype != torch.int32 or (parent.shape[1] > 1 and parent.stride(1) != 1):
+    if parent.dtype != _I32 or parent.dim() != 2 or (parent.stride(1) != 1 and parent.shape[1] > 1):
         raise ValueError(f"{what}: parent must be int32 [batch][beams]")
-    if parent.device != states.device:
-        raise ValueError(f"{what}: all tensors must be on one device")
     batch, beams = parent.shape
+    dev = states.device
+    if parent.get_device() != dev:
+        raise ValueError(f"{what}: all tensors must be on one CUDA device")
     if batch * beams != states.beams_total:
         raise ValueError(f"{what}: the states have {states.beams_total} beams, parent {batch} x {beams}")
-    with _Launch(what, states.device, stream) as s:
-        _check(lib.bc_beam_reorder(states.array, len(states.array), parent.data_ptr(),
-                                   parent.stride(0) if batch > 1 else beams, batch, beams, s),
-               "bc_beam_reorder")
+    other = _elsewhere(what, dev, stream)
+    if other is not None:
+        with other:
+            return beam_reorder(states, parent)
+    _check(lib.bc_beam_reorder(states.array, states.count, parent.data_ptr(),
+                               parent.stride(0) if batch > 1 else beams, batch, beams,
+                               _raw_stream(dev)), "bc_beam_reorder")
