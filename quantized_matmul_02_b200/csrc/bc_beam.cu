@@ -5,16 +5,20 @@
 //
 // ties going to the lowest w * V + v.
 //
-// Two launches, no atomics on results.  The first one reads the logits once:
-// a block owns one span of one beam's row, keeps a running maximum and sum of
-// exponentials, and the span's n_out best (logit, token) -- within a beam the
-// order by total is the order by logit.  The second one joins the spans of
-// each beam and selects over a request's beams.  HBM bound: 4 bytes per logit
-// against about ten operations.
+// Two launches.  The first one reads the logits once: a block owns one span of
+// one beam's row, keeps a reference near its maximum, the sum of exponentials, and the
+// span's n_out best (logit, token) -- within a beam the order by total is the
+// order by logit.  After its first tile a logit costs a comparison with the
+// n_out-th best so far.  The second one joins the spans of each beam and
+// selects over a request's beams.  HBM bound: 4 bytes per logit against about
+// seven operations.
 //
-// Precision: exponentials in fp32 relative to the running maximum, their sums
-// in fp64 (one addition per 8 elements), totals in fp64.  Order between beams
-// is decided on fp64 totals, so two candidates change places only where their
+// Keys (value, place) are all distinct, so the result does not depend on the
+// order in which candidates are collected.
+//
+// Precision: exponentials in fp32 relative to that reference, eight
+// added in fp32, the rest in fp64, totals in fp64.  Order between beams is
+// decided on fp64 totals, so two candidates change places only where their
 // totals agree to about 1e-7.
 #include "bc_internal.cuh"
 
@@ -22,56 +26,89 @@ namespace bc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 8;                          // logits per thread and tile
+constexpr int kWarps = kThreads / 32;
+constexpr int kPer = 16;                         // logits per thread and tile
 constexpr int kTile = kThreads * kPer;
 constexpr int64_t kSms = 148;
 constexpr int kMaxOut = 64;
 constexpr int kMaxBeams = 32;
-constexpr int kLimit = 192;                      // kept candidates before they are reduced
+constexpr int kLimit = kThreads;                 // kept candidates before they are reduced
 constexpr int kCap = kLimit + kTile;
+constexpr float kMax = 3.402823466e38f;
 
 // Order-preserving map of a float to an unsigned; -inf is kNegInf, and 0 is
-// below every value.  NaN counts as -inf (a masked token), +inf as the
-// largest finite value.
+// below every value.  The two zeros are one value.
 constexpr uint32_t kNegInf = 0x007fffffu;
 __device__ __forceinline__ uint32_t ord(float f) {
-    if (isnan(f)) return kNegInf;
-    const uint32_t u = __float_as_uint(fminf(f, 3.402823466e38f));
+    const uint32_t u = __float_as_uint(f + 0.f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float unord(uint32_t o) {
     return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 __device__ __forceinline__ uint64_t ord64(double d) {
-    const uint64_t u = (uint64_t)__double_as_longlong(d);
+    const uint64_t u = (uint64_t)__double_as_longlong(d + 0.0);
     return u & 0x8000000000000000ull ? ~u : u | 0x8000000000000000ull;
 }
 __device__ __forceinline__ double unord64(uint64_t o) {
     return __longlong_as_double((long long)(o & 0x8000000000000000ull ? o & 0x7fffffffffffffffull : ~o));
 }
+// NaN is a masked token, +inf the largest finite value.
+__device__ __forceinline__ float sane(float f) { return f <= kMax ? f : f > kMax ? kMax : -INFINITY; }
+__device__ __forceinline__ float exp2_fast(float f) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(f));
+    return r;
+}
+constexpr float kLog2e = 1.44269504f;
 
-// Keys: larger is better.  Logit key: (ord(logit), ~token); all are distinct.
+// Keys: larger is better, all are distinct.  Within a beam's row a key is
+// (ord(logit), ~token).
 struct SpanOut {
     double sum;                                  // sum of exp(logit - max)
-    float max;                                   // -inf when nothing is above -inf
+    float max;                                   // or near it; -inf when nothing is above -inf
     int count;                                   // keys that follow
 };
 
-// Leaves the `keep` largest of the n keys in buf[0..], sorted, and returns how
-// many there are.  All keys are distinct, so a key's rank is its place.
-__device__ __forceinline__ int reduce_keys(uint64_t *buf, uint64_t *tmp, int n, int keep) {
+// The n-th largest of the block's keys, one per thread: the largest T that n
+// of them reach, bit by bit from the top, and no further than needed to part
+// n of them from the rest.  0 when there are fewer than n (keys are above 0).
+__device__ __forceinline__ uint64_t nth_largest(uint64_t key, int n) {
+    uint64_t T = 0;
+    for (int b = 63; b >= 0; --b) {
+        const uint64_t c = T | 1ull << b;
+        const int reach = __syncthreads_count(key >= c);
+        if (reach >= n) T = c;
+        if (reach == n) break;
+    }
+    return T;
+}
+// The same for the m keys in buf (m > kThreads: each thread several).
+__device__ __forceinline__ uint64_t nth_largest(const uint64_t *buf, int m, int n, int *sums) {
+    constexpr int kMost = (kCap + kThreads - 1) / kThreads;
+    uint64_t k[kMost];
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int at = i * kThreads + threadIdx.x;
+        k[i] = at < m ? buf[at] : 0;
+    }
+    if (threadIdx.x < 64) sums[threadIdx.x] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const uint64_t k = buf[i];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += buf[j] > k;
-        if (rank < keep) tmp[rank] = k;
+    uint64_t T = 0;
+    for (int b = 63; b >= 0; --b) {
+        const uint64_t c = T | 1ull << b;
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) mine += k[i] >= c;
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if ((threadIdx.x & 31) == 0) atomicAdd(&sums[b], mine);
+        __syncthreads();
+        const int reach = sums[b];
+        if (reach >= n) T = c;
+        if (reach == n) break;
     }
     __syncthreads();
-    const int m = min(n, keep);
-    for (int i = threadIdx.x; i < m; i += kThreads) buf[i] = tmp[i];
-    __syncthreads();
-    return m;
+    return T;
 }
 
 struct SelectArgs {
@@ -83,7 +120,7 @@ struct SelectArgs {
     int64_t span;                                // logits per span, a multiple of kTile
     int32_t eos, pad;
     SpanOut *heads;                              // [rows][spans]
-    uint64_t *keys;                              // [rows][spans][n_out]
+    uint64_t *keys;                              // [rows][spans][n_out], each list in order
     float *out_scores;                           // [batch][n_out]
     int32_t *parent, *token;
     uint8_t *out_finished;
@@ -95,108 +132,149 @@ __device__ __forceinline__ bool idle(const SelectArgs &a, int64_t r) {
     return (a.finished && a.finished[r]) || isnan(s) || s == -INFINITY;
 }
 
-__device__ __forceinline__ double block_sum(double v, double *sh) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) v += sh[i];
-    return v;
-}
-
-// grid (spans, rows)
-__global__ void __launch_bounds__(kThreads) beam_span_kernel(const SelectArgs a) {
+// grid: rows x spans.  Places u of a row count from the 16-byte boundary at or
+// before its first logit (token = u - skip), so that any V reads whole words.
+__global__ void __launch_bounds__(kThreads, 3) beam_span_kernel(const SelectArgs a) {
     __shared__ uint64_t buf[kCap];
     __shared__ uint64_t tmp[kMaxOut];
-    __shared__ uint32_t tops[kThreads];
-    __shared__ double dsh[kThreads / 32];
-    __shared__ float fsh[kThreads / 32];
+    __shared__ double dsh[kWarps];
+    __shared__ float fsh[kWarps];
+    __shared__ int sums[64];
     __shared__ int count;
-    __shared__ uint32_t floor_sh;
-    const int64_t r = blockIdx.y;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t r = blockIdx.x / a.spans;
+    const int sp = (int)(blockIdx.x - r * a.spans);
     if (idle(a, r)) return;
     const float *row = a.logits + r * a.V;
-    const int64_t v0 = blockIdx.x * a.span, v1 = min(a.V, v0 + a.span);
-    const bool vec = (a.V & 3) == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
+    const int skip = (int)(reinterpret_cast<uintptr_t>(row) >> 2 & 3);
+    const int64_t end = a.V + skip, u0 = sp * a.span, u1 = min(end, u0 + a.span);
+    row -= skip;                                 // (never read before its first logit)
     const int tid = threadIdx.x;
     if (tid == 0) count = 0;
-    float m = -INFINITY;
+    float m = -INFINITY, floor = -INFINITY;      // logits have to be above the floor ...
+    bool open = true;                            // ... once there is one
     double sum = 0;
-    uint32_t floor = 0;                          // a key has to be above this to be kept
-    __syncthreads();
-    for (int64_t t0 = v0; t0 < v1; t0 += kTile) {
-        uint32_t o[kPer];
-        int64_t at[kPer];
+    auto load = [&](int64_t t0, float (&x)[kPer]) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            at[i] = vec ? t0 + (i / 4 * kThreads + tid) * 4 + (i & 3) : t0 + i * kThreads + tid;
-        if (vec) {
+        for (int i = 0; i < kPer; i += 4) {
+            const int64_t u = t0 + (i / 4 * kThreads + tid) * 4;
+            if (u >= skip && u + 4 <= u1) {
+                const float4 f = __ldcs(reinterpret_cast<const float4 *>(row + u));
+                x[i] = f.x;
+                x[i + 1] = f.y;
+                x[i + 2] = f.z;
+                x[i + 3] = f.w;
+            } else {
 #pragma unroll
-            for (int i = 0; i < kPer; i += 4) {
-                float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                if (at[i] < v1) f = __ldcs(reinterpret_cast<const float4 *>(row + at[i]));
-                o[i] = ord(f.x);
-                o[i + 1] = ord(f.y);
-                o[i + 2] = ord(f.z);
-                o[i + 3] = ord(f.w);
+                for (int e = 0; e < 4; ++e)
+                    x[i + e] = u + e >= skip && u + e < u1 ? __ldcs(row + u + e) : -INFINITY;
             }
-        } else {
-            float f[kPer];
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) f[i] = at[i] < v1 ? __ldcs(row + at[i]) : -INFINITY;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) o[i] = ord(f[i]);
         }
-        uint32_t top = 0;
+    };
+    auto place = [&](int64_t t0, int i) { return t0 + (i / 4 * kThreads + tid) * 4 + (i & 3); };
+    auto key = [&](float x, int64_t u) { return (uint64_t)ord(x) << 32 | (uint32_t)~(uint32_t)(u - skip); };
+    float next[kPer];
+    load(u0, next);
+    for (int64_t t0 = u0; t0 < u1; t0 += kTile) {
+        float x[kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (at[i] >= v1) o[i] = 0;
-            top = max(top, o[i]);
-        }
-        if (top > kNegInf) {
-            const float tm = unord(top);
-            if (tm > m) {
-                sum *= (double)expf(m - tm);
-                m = tm;
+        for (int i = 0; i < kPer; ++i) x[i] = next[i];
+        if (t0 + kTile < u1) load(t0 + kTile, next);
+        float total = x[0], top;
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) total += x[i];
+        if (!(total < INFINITY))                 // a NaN or +inf among them, or very large ones
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) x[i] = sane(x[i]);
+        top = x[0];
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
+        if (top > -INFINITY) {
+            // the reference follows a larger maximum only when it has to: sums of
+            // values up to exp(16) are as exact, and a change costs an fp64 exponential
+            if (top > m + 16.f || m == -INFINITY) {
+                sum *= exp((double)m - (double)top);
+                m = top;
             }
-            float s = 0.f;
+            float s[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (o[i] > kNegInf) s += expf(unord(o[i]) - m);
-            sum += (double)s;
+            for (int i = 0; i < kPer; ++i) s[i & 1] += exp2_fast((x[i] - m) * kLog2e);
+            sum += (double)s[0] + (double)s[1];
         }
-        if (t0 == v0) {
-            // first tile: the n_out-th largest of the threads' best values.
-            // At least n_out elements reach it, at most n_out * kPer + ties.
-            tops[tid] = top;
-            __syncthreads();
-            int above = 0, same = 0;
-            for (int j = 0; j < kThreads; ++j) {
-                above += tops[j] > top;
-                same += tops[j] == top && j < tid;
+        uint64_t least = 1;
+        if (t0 == u0) {
+            // First tile: the n_out-th largest of the threads' best keys; at most
+            // n_out threads have keys that reach it.
+            uint64_t best = 0;
+#pragma unroll
+            for (int i = kPer - 1; i >= 0; --i) {
+                const int64_t u = place(t0, i);
+                if (x[i] == top && u >= skip && u < u1) best = key(x[i], u);
             }
-            if (above + same == a.n_out - 1) floor_sh = top == 0 ? 0 : top - 1;
-            __syncthreads();
-            floor = floor_sh;
+            least = nth_largest(best, a.n_out);
+            if (least > 1) {                     // n_out keys reach it: later equals lose to them
+                open = false;
+                floor = unord(max((uint32_t)(least >> 32), kNegInf));
+            } else {
+                least = 1;
+            }
         }
+        // (the first tile's own keys at the floor are told apart by `least`)
+        const bool first = t0 == u0;
+        if (__syncthreads_or(first || open || top > floor)) {
+            if (first || open || top > floor) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (o[i] > floor)
-                buf[atomicAdd(&count, 1)] = (uint64_t)o[i] << 32 | (uint32_t)~(uint32_t)at[i];
-        __syncthreads();
-        const int held = count;
-        __syncthreads();                         // before the next tile counts on
-        if (held > kLimit) {
-            const int n = reduce_keys(buf, tmp, held, a.n_out);
-            // later tokens with the same logit come after the kept ones
-            if (n == a.n_out) floor = max(floor, (uint32_t)(buf[n - 1] >> 32));
-            if (tid == 0) count = n;
+                for (int i = 0; i < kPer; ++i) {
+                    const int64_t u = place(t0, i);
+                    if (u < skip || u >= u1) continue;
+                    if (first ? key(x[i], u) >= least : open || x[i] > floor)
+                        buf[atomicAdd(&count, 1)] = key(x[i], u);
+                }
+            }
             __syncthreads();
+            const int held = count;
+            __syncthreads();                     // before anyone counts on
+            if (held > kLimit) {
+                const uint64_t T = nth_largest(buf, held, a.n_out, sums);
+                if (tid == 0) count = 0;
+                __syncthreads();
+                for (int i = tid; i < held; i += kThreads)
+                    if (buf[i] >= T) tmp[atomicAdd(&count, 1)] = buf[i];
+                __syncthreads();
+                if (tid < a.n_out) buf[tid] = tmp[tid];          // n_out of them: held is above kLimit
+                // the floor is the least kept logit (T may have stopped short of its last bits)
+                uint32_t low = tid < a.n_out ? (uint32_t)(tmp[tid] >> 32) : 0xffffffffu;
+                low = __reduce_min_sync(0xffffffffu, low);
+                if ((tid & 31) == 0) fsh[tid >> 5] = unord(low);
+                __syncthreads();
+                floor = fminf(fsh[0], fsh[1]);                   // n_out <= 64: two warps
+                open = false;
+                __syncthreads();
+            }
         }
     }
-    const int n = reduce_keys(buf, tmp, count, a.n_out);
+    __syncthreads();
+    int n = count;
+    __syncthreads();
+    if (n > kThreads) {
+        const uint64_t T = nth_largest(buf, n, a.n_out, sums);
+        if (tid == 0) count = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads)
+            if (buf[i] >= T) tmp[atomicAdd(&count, 1)] = buf[i];
+        __syncthreads();
+        if (tid < a.n_out) buf[tid] = tmp[tid];
+        n = a.n_out;
+        __syncthreads();
+    }
+    // in order: a key's rank is its place
+    const int64_t at = r * a.spans + sp;
+    if (tid < n) {
+        const uint64_t k = buf[tid];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += buf[j] > k;
+        if (rank < a.n_out) a.keys[at * a.n_out + rank] = k;
+    }
     // one maximum and sum for the span
     float bm = m;
 #pragma unroll
@@ -204,35 +282,66 @@ __global__ void __launch_bounds__(kThreads) beam_span_kernel(const SelectArgs a)
     if ((tid & 31) == 0) fsh[tid >> 5] = bm;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) bm = fmaxf(bm, fsh[i]);
-    const double s = block_sum(m == -INFINITY ? 0.0 : sum * exp((double)m - (double)bm), dsh);
-    const int64_t at = r * a.spans + blockIdx.x;
-    if (tid == 0) a.heads[at] = SpanOut{s, bm, n};
-    for (int i = tid; i < n; i += kThreads) a.keys[at * a.n_out + i] = buf[i];
+    for (int i = 0; i < kWarps; ++i) bm = fmaxf(bm, fsh[i]);
+    double s = m == -INFINITY ? 0.0 : sum * exp((double)m - (double)bm);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if ((tid & 31) == 0) dsh[tid >> 5] = s;
+    __syncthreads();
+    if (tid == 0) {
+        s = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) s += dsh[i];
+        a.heads[at] = SpanOut{s, bm, min(n, a.n_out)};
+    }
 }
 
-// Request-wide keys: (ord64(total), ~(w * V + v)).
+// Request-wide keys: (ord64(total), ~(w * V + v)); all are distinct, 0 is none.
 struct Key {
     uint64_t hi;
     uint32_t lo;
 };
-__device__ __forceinline__ bool above(const Key &a, const Key &b) {
-    return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
+__device__ __forceinline__ bool reaches(const Key &a, const Key &b) {
+    return a.hi > b.hi || (a.hi == b.hi && a.lo >= b.lo);
+}
+// The n-th largest of the block's keys, P per thread (none: a key of 0).
+template <int P>
+__device__ __forceinline__ Key nth_largest(const Key (&k)[P], int n, int *sums) {
+    if (threadIdx.x < 96) sums[threadIdx.x] = 0;
+    __syncthreads();
+    Key T{0, 0};
+    for (int b = 95; b >= 0; --b) {
+        Key c = T;
+        if (b >= 32) c.hi |= 1ull << (b - 32);
+        else c.lo |= 1u << b;
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) mine += reaches(k[i], c);
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if ((threadIdx.x & 31) == 0 && mine) atomicAdd(&sums[b], mine);
+        __syncthreads();
+        const int reach = sums[b];
+        if (reach >= n) T = c;
+        if (reach == n) break;
+    }
+    __syncthreads();
+    return T;
 }
 
-constexpr int kJoinCap = 256 + kThreads;
+constexpr int kMaxLists = 6 * kThreads;          // a request's spans: at most 8 * kSms + kMaxBeams
 
 // one block per request
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const SelectArgs a) {
-    __shared__ Key buf[kJoinCap];
-    __shared__ Key tmp[kMaxOut];
-    __shared__ double lse[kMaxBeams];
-    __shared__ double score[kMaxBeams];
+    __shared__ Key kept[kMaxOut];
+    __shared__ int picked[kMaxOut];
+    __shared__ double lse[kMaxBeams], score[kMaxBeams];
     __shared__ uint8_t kind[kMaxBeams];          // 0: by its logits, 1: finished, 2: without a score
+    __shared__ int sums[96];
     __shared__ int count;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t b = blockIdx.x;
-    for (int w = warp; w < a.beams; w += kThreads / 32) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int w = warp; w < a.beams; w += kWarps) {
         const int64_t r = b * a.beams + w;
         const float sc = a.scores[r];
         const bool dead = isnan(sc) || sc == -INFINITY;
@@ -241,87 +350,115 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const SelectArgs a)
         float m = -INFINITY;
         if (!dead && !fin) {
             const SpanOut *h = a.heads + r * a.spans;
-            for (int i = lane; i < a.spans; i += 32) m = fmaxf(m, h[i].max);
+            for (int i = lane; i < a.spans; i += 32) {
+                const SpanOut o = h[i];
+                if (o.max > m) {
+                    s = s * exp((double)m - (double)o.max) + o.sum;
+                    m = o.max;
+                } else if (o.max > -INFINITY) {
+                    s += o.sum * exp((double)o.max - (double)m);
+                }
+            }
+            float bm = m;
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            if (m > -INFINITY)
-                for (int i = lane; i < a.spans; i += 32)
-                    s += h[i].sum * exp((double)h[i].max - (double)m);
+            for (int off = 16; off > 0; off >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, off));
+            s = m > -INFINITY ? s * exp((double)m - (double)bm) : 0.0;
+            m = bm;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
         }
         if (lane == 0) {
             kind[w] = dead ? 2 : fin ? 1 : m == -INFINITY ? 2 : 0;
-            lse[w] = kind[w] == 0 ? (double)m + log(s) : 0.0;
-            score[w] = (double)fminf(sc, 3.402823466e38f);
+            lse[w] = m > -INFINITY ? (double)m + log(s) : 0.0;
+            score[w] = (double)fminf(sc, kMax);
         }
     }
     if (tid == 0) count = 0;
     __syncthreads();
-    // candidates: best entries of all lists first, so that the floor rises early
-    const int lists = a.beams * a.spans;
-    const int64_t cands = (int64_t)lists * a.n_out;
-    Key floor{0, 0};
     const uint64_t none = ord64(-INFINITY);
-    for (int64_t c0 = 0; c0 < cands; c0 += kThreads) {
-        const int64_t c = c0 + tid;
+    // entry `rank` of a list, in descending order; lists are spans, or all of a
+    // beam that does not go by its logits (at its first span)
+    auto entry = [&](int list, int rank) {
+        const int w = list / a.spans, sp = list - w * a.spans;
+        const uint32_t base = (uint32_t)(w * a.V);
         Key k{0, 0};
-        if (c < cands) {
-            const int rank = (int)(c / lists), list = (int)(c % lists);
-            const int w = list / a.spans, sp = list % a.spans;
-            const uint32_t base = (uint32_t)(w * a.V);
+        if (kind[w] == 0) {
             const int64_t at = (b * a.beams + w) * a.spans + sp;
-            if (kind[w] == 0) {
-                if (rank < a.heads[at].count) {
-                    const uint64_t key = a.keys[at * a.n_out + rank];
-                    const uint32_t o = (uint32_t)(key >> 32);
-                    k.hi = o <= kNegInf ? none : ord64(score[w] + ((double)unord(o) - lse[w]));
-                    k.lo = ~(base + ~(uint32_t)key);
-                }
-            } else if (sp == 0) {
-                // nothing but -inf: the lowest tokens; a finished beam's pad token keeps its score
-                if (rank < a.V) {
-                    k.hi = none;
-                    k.lo = ~(base + (uint32_t)rank);
-                    const bool fin = kind[w] == 1;
-                    if (fin && rank == a.pad) k.hi = ord64(score[w]);
-                    if (fin && a.pad >= a.n_out && rank == a.n_out - 1) {
-                        k.hi = ord64(score[w]);
-                        k.lo = ~(base + (uint32_t)a.pad);
-                    }
-                }
+            if (rank < a.heads[at].count) {
+                const uint64_t key = a.keys[at * a.n_out + rank];
+                const uint32_t o = (uint32_t)(key >> 32);
+                k.hi = o <= kNegInf ? none : ord64(score[w] + ((double)unord(o) - lse[w]));
+                k.lo = ~(base + ~(uint32_t)key);
             }
-        }
-        if (above(k, floor)) buf[atomicAdd(&count, 1)] = k;
-        __syncthreads();
-        const int n = count;
-        if (n > 256 || c0 + kThreads >= cands) {
-            for (int i = tid; i < n; i += kThreads) {
-                const Key x = buf[i];
-                int rank = 0;
-                for (int j = 0; j < n; ++j) rank += above(buf[j], x);
-                if (rank < a.n_out) tmp[rank] = x;
+        } else if (sp == 0 && rank < a.V) {
+            // nothing but -inf, by the lowest tokens; first a finished beam's pad token at its score
+            int64_t v = rank;
+            k.hi = none;
+            if (kind[w] == 1) {
+                if (rank == 0) k.hi = ord64(score[w]);
+                v = rank == 0 ? a.pad : rank - 1 + (rank - 1 >= a.pad);
             }
-            __syncthreads();
-            const int kept = min(n, a.n_out);
-            for (int i = tid; i < kept; i += kThreads) buf[i] = tmp[i];
-            if (tid == 0) count = kept;
-            __syncthreads();
-            if (kept == a.n_out) floor = buf[kept - 1];
+            k.lo = ~(base + (uint32_t)v);
         }
+        return k;
+    };
+    // the n_out lists with the best first entries hold all that can be chosen
+    const int lists = a.beams * a.spans;
+    int n_picked = lists;
+    if (lists > a.n_out) {
+        Key h[kMaxLists / kThreads];
+#pragma unroll
+        for (int i = 0; i < kMaxLists / kThreads; ++i) {
+            const int l = i * kThreads + tid;
+            h[i] = l < lists ? entry(l, 0) : Key{0, 0};
+        }
+        const Key T = nth_largest(h, a.n_out, sums);
+#pragma unroll
+        for (int i = 0; i < kMaxLists / kThreads; ++i)
+            if (h[i].hi && reaches(h[i], T)) picked[atomicAdd(&count, 1)] = i * kThreads + tid;
         __syncthreads();
+        n_picked = count;
+    } else if (tid < lists) {
+        picked[tid] = tid;
     }
-    for (int i = tid; i < a.n_out; i += kThreads) {
-        const Key k = buf[i];
+    __syncthreads();
+    if (tid == 0) count = 0;
+    const int cands = n_picked * a.n_out;
+    auto finish = [&](auto &k) {                 // k: this thread's candidates
+        const Key T = nth_largest(k, a.n_out, sums);
+        for (const Key &x : k)
+            if (x.hi && reaches(x, T)) kept[atomicAdd(&count, 1)] = x;
+    };
+    auto gather = [&](auto &k) {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(k) / sizeof(k[0])); ++i) {
+            const int c = i * kThreads + tid, l = c / a.n_out;
+            k[i] = c < cands ? entry(picked[l], c - l * a.n_out) : Key{0, 0};
+        }
+    };
+    if (cands <= kThreads) {
+        Key k[1];
+        gather(k);
+        finish(k);
+    } else {
+        Key k[kMaxOut * kMaxOut / kThreads];
+        gather(k);
+        finish(k);
+    }
+    __syncthreads();
+    if (tid < a.n_out) {
+        const Key k = kept[tid];
+        int rank = -1;
+        for (int j = 0; j < a.n_out; ++j) rank += reaches(kept[j], k);
         const uint32_t flat = ~k.lo;
         const int w = (int)(flat / (uint32_t)a.V);
         const int32_t t = (int32_t)(flat - (uint32_t)(w * a.V));
-        const int64_t at = b * a.n_out + i;
+        const int64_t at = b * a.n_out + rank;
         a.out_scores[at] = (float)unord64(k.hi);
         a.parent[at] = w;
         a.token[at] = t;
         if (a.out_finished)
-            a.out_finished[at] = (kind[w] == 1 || (a.finished && a.finished[b * a.beams + w]) || t == a.eos) ? 1 : 0;
+            a.out_finished[at] = ((a.finished && a.finished[b * a.beams + w]) || t == a.eos) ? 1 : 0;
     }
 }
 
@@ -330,7 +467,7 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 // Spans per row: enough blocks to fill the GPU several times over, none
 // shorter than one tile.
 int spans_of(int64_t rows, int64_t V) {
-    const int64_t tiles = (V + kTile - 1) / kTile;
+    const int64_t tiles = (V + 3 + kTile - 1) / kTile;
     int64_t want = (8 * kSms + rows - 1) / rows;
     if (want > tiles) want = tiles;
     if (want < 1) want = 1;
@@ -400,7 +537,7 @@ bc_status bc_beam_select(const float *logits, const float *scores, const uint8_t
     a.beams = (int)beams;
     a.n_out = (int)n_out;
     a.spans = spans_of((int64_t)rows, V);
-    const int64_t tiles = (V + kTile - 1) / kTile;
+    const int64_t tiles = (V + 3 + kTile - 1) / kTile;
     a.span = (tiles + a.spans - 1) / a.spans * kTile;
     a.eos = eos;
     a.pad = finished ? pad : 0;
@@ -412,9 +549,24 @@ bc_status bc_beam_select(const float *logits, const float *scores, const uint8_t
     a.token = token;
     a.out_finished = out_finished;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    beam_span_kernel<<<dim3((unsigned)a.spans, (unsigned)rows), kThreads, 0, s>>>(a);
-    beam_join_kernel<<<(unsigned)batch, kThreads, 0, s>>>(a);
-    return cuda_status();
+    beam_span_kernel<<<(unsigned)(rows * a.spans), kThreads, 0, s>>>(a);
+    st = cuda_status();
+    if (st != BC_OK) return st;
+    // the second kernel's blocks may start while the first one's finish; they wait for all of it
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)batch);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, beam_join_kernel, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return BC_ERR_CUDA;
+    }
+    return BC_OK;
 }
 
 size_t bc_workspace_size_matmul_beam(int64_t batch, int64_t beams, int64_t N, int64_t K,
