@@ -70,45 +70,81 @@ struct SpanOut {
     int count;                                   // keys that follow
 };
 
-// The n-th largest of the block's keys, one per thread: the largest T that n
-// of them reach, bit by bit from the top, and no further than needed to part
-// n of them from the rest.  0 when there are fewer than n (keys are above 0).
-__device__ __forceinline__ uint64_t nth_largest(uint64_t key, int n) {
-    uint64_t T = 0;
-    for (int b = 63; b >= 0; --b) {
-        const uint64_t c = T | 1ull << b;
-        const int reach = __syncthreads_count(key >= c);
-        if (reach >= n) T = c;
-        if (reach == n) break;
-    }
-    return T;
-}
-// The same for the m keys in buf (m > kThreads: each thread several).
-__device__ __forceinline__ uint64_t nth_largest(const uint64_t *buf, int m, int n, int *sums) {
-    constexpr int kMost = (kCap + kThreads - 1) / kThreads;
-    uint64_t k[kMost];
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-        const int at = i * kThreads + threadIdx.x;
-        k[i] = at < m ? buf[at] : 0;
-    }
-    if (threadIdx.x < 64) sums[threadIdx.x] = 0;
-    __syncthreads();
-    uint64_t T = 0;
-    for (int b = 63; b >= 0; --b) {
-        const uint64_t c = T | 1ull << b;
-        int mine = 0;
-#pragma unroll
-        for (int i = 0; i < kMost; ++i) mine += k[i] >= c;
-        mine = __reduce_add_sync(0xffffffffu, mine);
-        if ((threadIdx.x & 31) == 0) atomicAdd(&sums[b], mine);
+// The n largest of the block's keys, P per thread of W 32-bit words (most
+// significant first, all distinct; a first word of 0 is no key): a mask of this
+// thread's among them, all of them when there are no more than n.  Word by
+// word and bit by bit from the highest bit in which the keys differ, no
+// further than needed to part n of them from the rest.
+struct ChooseShared {
+    int sums[34 * 3 + 2];
+    uint32_t most[kWarps], least[kWarps];
+};
+template <int P, int W>
+__device__ __forceinline__ uint32_t choose(const uint32_t (&k)[P][W], int n, ChooseShared &sh) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int slot = 0;
+    if constexpr (P > 1) {
+        if (tid < (int)(sizeof(sh.sums) / 4)) sh.sums[tid] = 0;
         __syncthreads();
-        const int reach = sums[b];
-        if (reach >= n) T = c;
-        if (reach == n) break;
     }
-    __syncthreads();
-    return T;
+    auto count = [&](uint32_t mask) {
+        if constexpr (P == 1) return __syncthreads_count(mask);
+        const int c = __reduce_add_sync(0xffffffffu, __popc(mask));
+        if (lane == 0 && c) atomicAdd(&sh.sums[slot], c);
+        __syncthreads();
+        return sh.sums[slot++];
+    };
+    uint32_t active = 0, chosen = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) active |= (uint32_t)(k[i][0] != 0) << i;
+    if (count(active) <= n) return active;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        uint32_t hi = 0, lo = 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (active >> i & 1) {
+                hi = max(hi, k[i][w]);
+                lo = min(lo, k[i][w]);
+            }
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        if (lane == 0) {
+            sh.most[warp] = hi;
+            sh.least[warp] = lo;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            hi = max(hi, sh.most[i]);
+            lo = min(lo, sh.least[i]);
+        }
+        if (hi != lo) {
+            int b = 31 - __clz(hi ^ lo);
+            uint32_t T = hi & ~((2u << b) - 1);
+            auto above = [&](uint32_t c) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < P; ++i) m |= (uint32_t)(k[i][w] >= c) << i;
+                return m & active;
+            };
+            for (; b >= 0; --b) {
+                const uint32_t m = above(T | 1u << b);
+                const int reach = count(m);
+                if (reach == n) return chosen | m;
+                if (reach > n) T |= 1u << b;
+            }
+            // T is the n-th's word: those above it are in, those equal to it go on
+            const uint32_t over = T == 0xffffffffu ? 0 : above(T + 1);
+            n -= count(over);
+            chosen |= over;
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                if (k[i][w] != T) active &= ~(1u << i);
+        }
+        __syncthreads();                         // most[] and least[] are free
+    }
+    return chosen;
 }
 
 struct SelectArgs {
@@ -117,7 +153,7 @@ struct SelectArgs {
     const uint8_t *finished;                     // [batch][beams] or null
     int64_t V;
     int beams, n_out, spans;
-    int64_t span;                                // logits per span, a multiple of kTile
+    int span;                                    // logits per span, a multiple of kTile
     int32_t eos, pad;
     SpanOut *heads;                              // [rows][spans]
     uint64_t *keys;                              // [rows][spans][n_out], each list in order
@@ -137,9 +173,9 @@ __device__ __forceinline__ bool idle(const SelectArgs &a, int64_t r) {
 __global__ void __launch_bounds__(kThreads, 3) beam_span_kernel(const SelectArgs a) {
     __shared__ uint64_t buf[kCap];
     __shared__ uint64_t tmp[kMaxOut];
+    __shared__ ChooseShared cs;
     __shared__ double dsh[kWarps];
     __shared__ float fsh[kWarps];
-    __shared__ int sums[64];
     __shared__ int count;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t r = blockIdx.x / a.spans;
@@ -147,35 +183,66 @@ __global__ void __launch_bounds__(kThreads, 3) beam_span_kernel(const SelectArgs
     if (idle(a, r)) return;
     const float *row = a.logits + r * a.V;
     const int skip = (int)(reinterpret_cast<uintptr_t>(row) >> 2 & 3);
-    const int64_t end = a.V + skip, u0 = sp * a.span, u1 = min(end, u0 + a.span);
+    const int u0 = sp * a.span, u1 = min((int)a.V + skip, u0 + a.span);
     row -= skip;                                 // (never read before its first logit)
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, n_out = a.n_out;
     if (tid == 0) count = 0;
     float m = -INFINITY, floor = -INFINITY;      // logits have to be above the floor ...
     bool open = true;                            // ... once there is one
     double sum = 0;
-    auto load = [&](int64_t t0, float (&x)[kPer]) {
+    auto inside = [&](int t0) { return t0 >= skip && t0 + kTile <= u1; };
+    auto place = [&](int t0, int i) { return t0 + (i / 4 * kThreads + tid) * 4 + (i & 3); };
+    auto load = [&](int t0, float (&x)[kPer]) {
+        if (inside(t0)) {
+            const float4 *p = reinterpret_cast<const float4 *>(row + t0) + tid;
 #pragma unroll
-        for (int i = 0; i < kPer; i += 4) {
-            const int64_t u = t0 + (i / 4 * kThreads + tid) * 4;
-            if (u >= skip && u + 4 <= u1) {
-                const float4 f = __ldcs(reinterpret_cast<const float4 *>(row + u));
+            for (int i = 0; i < kPer; i += 4) {
+                const float4 f = __ldcs(p + i / 4 * kThreads);
                 x[i] = f.x;
                 x[i + 1] = f.y;
                 x[i + 2] = f.z;
                 x[i + 3] = f.w;
-            } else {
+            }
+        } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[i + e] = u + e >= skip && u + e < u1 ? __ldcs(row + u + e) : -INFINITY;
+            for (int i = 0; i < kPer; ++i) {
+                const int u = place(t0, i);
+                x[i] = u >= skip && u < u1 ? __ldcs(row + u) : -INFINITY;
             }
         }
     };
-    auto place = [&](int64_t t0, int i) { return t0 + (i / 4 * kThreads + tid) * 4 + (i & 3); };
-    auto key = [&](float x, int64_t u) { return (uint64_t)ord(x) << 32 | (uint32_t)~(uint32_t)(u - skip); };
+    // The n_out largest of buf's keys (more than n_out) move to its front, in no order.
+    auto reduce = [&](int held) {
+        auto move = [&](auto &k) {
+            constexpr int P = sizeof(k) / sizeof(k[0]);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int at = i * kThreads + tid;
+                const uint64_t key = at < held ? buf[at] : 0;
+                k[i][0] = (uint32_t)(key >> 32);
+                k[i][1] = (uint32_t)key;
+            }
+            const uint32_t mine = choose(k, n_out, cs);
+            if (tid == 0) count = 0;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                if (mine >> i & 1) tmp[atomicAdd(&count, 1)] = (uint64_t)k[i][0] << 32 | k[i][1];
+        };
+        if (held <= kThreads) {
+            uint32_t k[1][2];
+            move(k);
+        } else {
+            uint32_t k[(kCap + kThreads - 1) / kThreads][2];
+            move(k);
+        }
+        __syncthreads();
+        if (tid < n_out) buf[tid] = tmp[tid];
+        __syncthreads();
+    };
     float next[kPer];
     load(u0, next);
-    for (int64_t t0 = u0; t0 < u1; t0 += kTile) {
+    for (int t0 = u0; t0 < u1; t0 += kTile) {
         float x[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) x[i] = next[i];
@@ -201,53 +268,54 @@ __global__ void __launch_bounds__(kThreads, 3) beam_span_kernel(const SelectArgs
             for (int i = 0; i < kPer; ++i) s[i & 1] += exp2_fast((x[i] - m) * kLog2e);
             sum += (double)s[0] + (double)s[1];
         }
-        uint64_t least = 1;
-        if (t0 == u0) {
-            // First tile: the n_out-th largest of the threads' best keys; at most
-            // n_out threads have keys that reach it.
-            uint64_t best = 0;
+        const bool first = t0 == u0;
+        float bar = floor;                       // candidates reach it (first tile), or are above it
+        if (first) {
+            // the n_out-th largest of the threads' best logits: n_out of them reach it
+            bool any = place(t0, kPer - 4) < u1 && place(t0, kPer - 1) >= skip;
+            if (!any)
 #pragma unroll
-            for (int i = kPer - 1; i >= 0; --i) {
-                const int64_t u = place(t0, i);
-                if (x[i] == top && u >= skip && u < u1) best = key(x[i], u);
-            }
-            least = nth_largest(best, a.n_out);
-            if (least > 1) {                     // n_out keys reach it: later equals lose to them
+                for (int i = 0; i < kPer; ++i) any |= place(t0, i) >= skip && place(t0, i) < u1;
+            const uint32_t k[1][1] = {{any ? ord(top) : 0}};
+            const uint32_t mine = choose(k, n_out, cs);
+            if (__syncthreads_count(k[0][0] != 0) >= n_out) {
+                // (equal logits may leave `mine` short of n_out: then all that equal the rest are wanted)
+                const int got = __syncthreads_count(mine);
+                uint32_t low = got == n_out ? (mine ? k[0][0] : 0xffffffffu)
+                                            : (mine || k[0][0] == 0 ? 0 : k[0][0]);
+                low = got == n_out ? __reduce_min_sync(0xffffffffu, low) : __reduce_max_sync(0xffffffffu, low);
+                if ((tid & 31) == 0) cs.most[tid >> 5] = low;
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i)
+                    low = got == n_out ? min(low, cs.most[i]) : max(low, cs.most[i]);
+                floor = unord(low);
+                bar = floor;
                 open = false;
-                floor = unord(max((uint32_t)(least >> 32), kNegInf));
-            } else {
-                least = 1;
             }
         }
-        // (the first tile's own keys at the floor are told apart by `least`)
-        const bool first = t0 == u0;
-        if (__syncthreads_or(first || open || top > floor)) {
-            if (first || open || top > floor) {
+        if (__syncthreads_or(first || open || top > bar)) {
+            if (first ? top >= bar : open || top > bar) {
+                const bool all = inside(t0);
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int64_t u = place(t0, i);
-                    if (u < skip || u >= u1) continue;
-                    if (first ? key(x[i], u) >= least : open || x[i] > floor)
-                        buf[atomicAdd(&count, 1)] = key(x[i], u);
-                }
+                for (int i = 0; i < kPer; ++i)
+                    if (first ? x[i] >= bar : open || x[i] > bar) {
+                        const int u = place(t0, i);
+                        if (all || (u >= skip && u < u1))
+                            buf[atomicAdd(&count, 1)] = (uint64_t)ord(x[i]) << 32 | (uint32_t)~(uint32_t)(u - skip);
+                    }
             }
             __syncthreads();
             const int held = count;
             __syncthreads();                     // before anyone counts on
             if (held > kLimit) {
-                const uint64_t T = nth_largest(buf, held, a.n_out, sums);
-                if (tid == 0) count = 0;
-                __syncthreads();
-                for (int i = tid; i < held; i += kThreads)
-                    if (buf[i] >= T) tmp[atomicAdd(&count, 1)] = buf[i];
-                __syncthreads();
-                if (tid < a.n_out) buf[tid] = tmp[tid];          // n_out of them: held is above kLimit
-                // the floor is the least kept logit (T may have stopped short of its last bits)
-                uint32_t low = tid < a.n_out ? (uint32_t)(tmp[tid] >> 32) : 0xffffffffu;
+                reduce(held);
+                // the floor is the least kept logit: later equals lose to it
+                uint32_t low = tid < n_out ? (uint32_t)(tmp[tid] >> 32) : 0xffffffffu;
                 low = __reduce_min_sync(0xffffffffu, low);
-                if ((tid & 31) == 0) fsh[tid >> 5] = unord(low);
+                if ((tid & 31) == 0) cs.most[tid >> 5] = low;
                 __syncthreads();
-                floor = fminf(fsh[0], fsh[1]);                   // n_out <= 64: two warps
+                floor = unord(min(cs.most[0], cs.most[1]));      // n_out <= 64: two warps
                 open = false;
                 __syncthreads();
             }
@@ -256,16 +324,9 @@ __global__ void __launch_bounds__(kThreads, 3) beam_span_kernel(const SelectArgs
     __syncthreads();
     int n = count;
     __syncthreads();
-    if (n > kThreads) {
-        const uint64_t T = nth_largest(buf, n, a.n_out, sums);
-        if (tid == 0) count = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += kThreads)
-            if (buf[i] >= T) tmp[atomicAdd(&count, 1)] = buf[i];
-        __syncthreads();
-        if (tid < a.n_out) buf[tid] = tmp[tid];
-        n = a.n_out;
-        __syncthreads();
+    if (n > 2 * kMaxOut || n > kThreads) {
+        reduce(n);
+        n = n_out;
     }
     // in order: a key's rank is its place
     const int64_t at = r * a.spans + sp;
@@ -273,9 +334,9 @@ __global__ void __launch_bounds__(kThreads, 3) beam_span_kernel(const SelectArgs
         const uint64_t k = buf[tid];
         int rank = 0;
         for (int j = 0; j < n; ++j) rank += buf[j] > k;
-        if (rank < a.n_out) a.keys[at * a.n_out + rank] = k;
+        if (rank < n_out) a.keys[at * n_out + rank] = k;
     }
-    // one maximum and sum for the span
+    // one reference and sum for the span
     float bm = m;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, off));
@@ -292,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 3) beam_span_kernel(const SelectArgs
         s = 0;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) s += dsh[i];
-        a.heads[at] = SpanOut{s, bm, min(n, a.n_out)};
+        a.heads[at] = SpanOut{s, bm, min(n, n_out)};
     }
 }
 
@@ -301,31 +362,19 @@ struct Key {
     uint64_t hi;
     uint32_t lo;
 };
-__device__ __forceinline__ bool reaches(const Key &a, const Key &b) {
-    return a.hi > b.hi || (a.hi == b.hi && a.lo >= b.lo);
+__device__ __forceinline__ bool above(const Key &a, const Key &b) {
+    return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
 }
-// The n-th largest of the block's keys, P per thread (none: a key of 0).
 template <int P>
-__device__ __forceinline__ Key nth_largest(const Key (&k)[P], int n, int *sums) {
-    if (threadIdx.x < 96) sums[threadIdx.x] = 0;
-    __syncthreads();
-    Key T{0, 0};
-    for (int b = 95; b >= 0; --b) {
-        Key c = T;
-        if (b >= 32) c.hi |= 1ull << (b - 32);
-        else c.lo |= 1u << b;
-        int mine = 0;
+__device__ __forceinline__ uint32_t choose(const Key (&k)[P], int n, ChooseShared &sh) {
+    uint32_t w[P][3];
 #pragma unroll
-        for (int i = 0; i < P; ++i) mine += reaches(k[i], c);
-        mine = __reduce_add_sync(0xffffffffu, mine);
-        if ((threadIdx.x & 31) == 0 && mine) atomicAdd(&sums[b], mine);
-        __syncthreads();
-        const int reach = sums[b];
-        if (reach >= n) T = c;
-        if (reach == n) break;
+    for (int i = 0; i < P; ++i) {
+        w[i][0] = (uint32_t)(k[i].hi >> 32);
+        w[i][1] = (uint32_t)k[i].hi;
+        w[i][2] = k[i].lo;
     }
-    __syncthreads();
-    return T;
+    return choose(w, n, sh);
 }
 
 constexpr int kMaxLists = 6 * kThreads;          // a request's spans: at most 8 * kSms + kMaxBeams
@@ -336,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const SelectArgs a)
     __shared__ int picked[kMaxOut];
     __shared__ double lse[kMaxBeams], score[kMaxBeams];
     __shared__ uint8_t kind[kMaxBeams];          // 0: by its logits, 1: finished, 2: without a score
-    __shared__ int sums[96];
+    __shared__ ChooseShared cs;
     __shared__ int count;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t b = blockIdx.x;
@@ -405,39 +454,43 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const SelectArgs a)
     // the n_out lists with the best first entries hold all that can be chosen
     const int lists = a.beams * a.spans;
     int n_picked = lists;
-    if (lists > a.n_out) {
+    if (lists * a.n_out > 4 * kThreads) {
         Key h[kMaxLists / kThreads];
 #pragma unroll
         for (int i = 0; i < kMaxLists / kThreads; ++i) {
             const int l = i * kThreads + tid;
             h[i] = l < lists ? entry(l, 0) : Key{0, 0};
         }
-        const Key T = nth_largest(h, a.n_out, sums);
+        const uint32_t mine = choose(h, a.n_out, cs);
 #pragma unroll
         for (int i = 0; i < kMaxLists / kThreads; ++i)
-            if (h[i].hi && reaches(h[i], T)) picked[atomicAdd(&count, 1)] = i * kThreads + tid;
+            if (mine >> i & 1) picked[atomicAdd(&count, 1)] = i * kThreads + tid;
         __syncthreads();
         n_picked = count;
-    } else if (tid < lists) {
-        picked[tid] = tid;
     }
+    const bool few = n_picked == lists;          // no lists were left out: they are numbered as they are
     __syncthreads();
     if (tid == 0) count = 0;
     const int cands = n_picked * a.n_out;
     auto finish = [&](auto &k) {                 // k: this thread's candidates
-        const Key T = nth_largest(k, a.n_out, sums);
-        for (const Key &x : k)
-            if (x.hi && reaches(x, T)) kept[atomicAdd(&count, 1)] = x;
+        const uint32_t mine = choose(k, a.n_out, cs);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(k) / sizeof(k[0])); ++i)
+            if (mine >> i & 1) kept[atomicAdd(&count, 1)] = k[i];
     };
     auto gather = [&](auto &k) {
 #pragma unroll
         for (int i = 0; i < (int)(sizeof(k) / sizeof(k[0])); ++i) {
             const int c = i * kThreads + tid, l = c / a.n_out;
-            k[i] = c < cands ? entry(picked[l], c - l * a.n_out) : Key{0, 0};
+            k[i] = c < cands ? entry(few ? l : picked[l], c - l * a.n_out) : Key{0, 0};
         }
     };
     if (cands <= kThreads) {
         Key k[1];
+        gather(k);
+        finish(k);
+    } else if (cands <= 4 * kThreads) {
+        Key k[4];
         gather(k);
         finish(k);
     } else {
@@ -448,8 +501,8 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const SelectArgs a)
     __syncthreads();
     if (tid < a.n_out) {
         const Key k = kept[tid];
-        int rank = -1;
-        for (int j = 0; j < a.n_out; ++j) rank += reaches(kept[j], k);
+        int rank = 0;
+        for (int j = 0; j < a.n_out; ++j) rank += above(kept[j], k);
         const uint32_t flat = ~k.lo;
         const int w = (int)(flat / (uint32_t)a.V);
         const int32_t t = (int32_t)(flat - (uint32_t)(w * a.V));
@@ -538,7 +591,7 @@ bc_status bc_beam_select(const float *logits, const float *scores, const uint8_t
     a.n_out = (int)n_out;
     a.spans = spans_of((int64_t)rows, V);
     const int64_t tiles = (V + 3 + kTile - 1) / kTile;
-    a.span = (tiles + a.spans - 1) / a.spans * kTile;
+    a.span = (int)((tiles + a.spans - 1) / a.spans * kTile);
     a.eos = eos;
     a.pad = finished ? pad : 0;
     a.heads = static_cast<SpanOut *>(workspace);
