@@ -240,91 +240,111 @@ __global__ void __launch_bounds__(kThreads, 3) beam_span_kernel(const SelectArgs
         if (tid < n_out) buf[tid] = tmp[tid];
         __syncthreads();
     };
-    float next[kPer];
-    load(u0, next);
-    for (int t0 = u0; t0 < u1; t0 += kTile) {
-        float x[kPer];
+    // Candidates are collected without waiting for one another, as far as buf
+    // goes; every `every` tiles they are reduced.  Logits that rise along the
+    // row can bring more: then the span is read again, with room for all of a
+    // tile before each.
+    int n = 0;
+    for (int every = 4;; every = 1) {
+        float next[kPer];
+        load(u0, next);
+        int tile = 0;
+        for (int t0 = u0; t0 < u1; t0 += kTile, ++tile) {
+            float x[kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = next[i];
-        if (t0 + kTile < u1) load(t0 + kTile, next);
-        float total = x[0], top;
+            for (int i = 0; i < kPer; ++i) x[i] = next[i];
+            if (t0 + kTile < u1) load(t0 + kTile, next);
+            float total = x[0], tops[kPer / 4];
 #pragma unroll
-        for (int i = 1; i < kPer; ++i) total += x[i];
-        if (!(total < INFINITY))                 // a NaN or +inf among them, or very large ones
+            for (int i = 1; i < kPer; ++i) total += x[i];
+            if (!(total < INFINITY))             // a NaN or +inf among them, or very large ones
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) x[i] = sane(x[i]);
-        top = x[0];
+                for (int i = 0; i < kPer; ++i) x[i] = sane(x[i]);
 #pragma unroll
-        for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
-        if (top > -INFINITY) {
-            // the reference follows a larger maximum only when it has to: sums of
-            // values up to exp(16) are as exact, and a change costs an fp64 exponential
-            if (top > m + 16.f || m == -INFINITY) {
-                sum *= exp((double)m - (double)top);
-                m = top;
+            for (int i = 0; i < kPer / 4; ++i)
+                tops[i] = fmaxf(fmaxf(x[4 * i], x[4 * i + 1]), fmaxf(x[4 * i + 2], x[4 * i + 3]));
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+            if (top > -INFINITY) {
+                // the reference follows a larger maximum only when it has to: sums of
+                // values up to exp(16) are as exact, and a change costs an fp64 exponential
+                if (top > m + 16.f || m == -INFINITY) {
+                    sum *= exp((double)m - (double)top);
+                    m = top;
+                }
+                float s[2] = {0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) s[i & 1] += exp2_fast((x[i] - m) * kLog2e);
+                sum += (double)s[0] + (double)s[1];
             }
-            float s[2] = {0.f, 0.f};
+            const bool first = tile == 0;
+            if (first) {
+                // the n_out-th largest of the threads' best logits: n_out of them reach it
+                bool any = false;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) s[i & 1] += exp2_fast((x[i] - m) * kLog2e);
-            sum += (double)s[0] + (double)s[1];
-        }
-        const bool first = t0 == u0;
-        float bar = floor;                       // candidates reach it (first tile), or are above it
-        if (first) {
-            // the n_out-th largest of the threads' best logits: n_out of them reach it
-            bool any = place(t0, kPer - 4) < u1 && place(t0, kPer - 1) >= skip;
-            if (!any)
+                for (int i = 0; i < kPer; i += 3) any |= place(t0, i) >= skip && place(t0, i) < u1;
+                const uint32_t k[1][1] = {{any ? ord(top) : 0}};
+                const uint32_t mine = choose(k, n_out, cs);
+                if (__syncthreads_count(k[0][0] != 0) >= n_out) {
+                    // (equal logits may leave `mine` short of n_out: then all that equal the rest are wanted)
+                    const int got = __syncthreads_count(mine);
+                    uint32_t low = got == n_out ? (mine ? k[0][0] : 0xffffffffu)
+                                                : (mine || k[0][0] == 0 ? 0 : k[0][0]);
+                    low = got == n_out ? __reduce_min_sync(0xffffffffu, low) : __reduce_max_sync(0xffffffffu, low);
+                    if ((tid & 31) == 0) cs.most[tid >> 5] = low;
+                    __syncthreads();
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) any |= place(t0, i) >= skip && place(t0, i) < u1;
-            const uint32_t k[1][1] = {{any ? ord(top) : 0}};
-            const uint32_t mine = choose(k, n_out, cs);
-            if (__syncthreads_count(k[0][0] != 0) >= n_out) {
-                // (equal logits may leave `mine` short of n_out: then all that equal the rest are wanted)
-                const int got = __syncthreads_count(mine);
-                uint32_t low = got == n_out ? (mine ? k[0][0] : 0xffffffffu)
-                                            : (mine || k[0][0] == 0 ? 0 : k[0][0]);
-                low = got == n_out ? __reduce_min_sync(0xffffffffu, low) : __reduce_max_sync(0xffffffffu, low);
-                if ((tid & 31) == 0) cs.most[tid >> 5] = low;
-                __syncthreads();
-#pragma unroll
-                for (int i = 0; i < kWarps; ++i)
-                    low = got == n_out ? min(low, cs.most[i]) : max(low, cs.most[i]);
-                floor = unord(low);
-                bar = floor;
-                open = false;
+                    for (int i = 0; i < kWarps; ++i)
+                        low = got == n_out ? min(low, cs.most[i]) : max(low, cs.most[i]);
+                    floor = unord(low);
+                    open = false;
+                }
             }
-        }
-        if (__syncthreads_or(first || open || top > bar)) {
-            if (first ? top >= bar : open || top > bar) {
+            // candidates reach the floor (first tile), or are above it: later equals lose
+            auto wanted = [&](float f) { return first ? f >= floor : open || f > floor; };
+            if (wanted(top)) {
                 const bool all = inside(t0);
 #pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (first ? x[i] >= bar : open || x[i] > bar) {
-                        const int u = place(t0, i);
-                        if (all || (u >= skip && u < u1))
-                            buf[atomicAdd(&count, 1)] = (uint64_t)ord(x[i]) << 32 | (uint32_t)~(uint32_t)(u - skip);
-                    }
+                for (int q = 0; q < kPer / 4; ++q)
+                    if (wanted(tops[q]))
+#pragma unroll
+                        for (int i = q * 4; i < q * 4 + 4; ++i)
+                            if (wanted(x[i])) {
+                                const int u = place(t0, i);
+                                if (all || (u >= skip && u < u1)) {
+                                    const int to = atomicAdd(&count, 1);
+                                    if (to < kCap) buf[to] = (uint64_t)ord(x[i]) << 32 | (uint32_t)~(uint32_t)(u - skip);
+                                }
+                            }
             }
-            __syncthreads();
-            const int held = count;
-            __syncthreads();                     // before anyone counts on
-            if (held > kLimit) {
-                reduce(held);
-                // the floor is the least kept logit: later equals lose to it
-                uint32_t low = tid < n_out ? (uint32_t)(tmp[tid] >> 32) : 0xffffffffu;
-                low = __reduce_min_sync(0xffffffffu, low);
-                if ((tid & 31) == 0) cs.most[tid >> 5] = low;
+            if (tile % every == every - 1) {
                 __syncthreads();
-                floor = unord(min(cs.most[0], cs.most[1]));      // n_out <= 64: two warps
-                open = false;
-                __syncthreads();
+                const int held = count;
+                __syncthreads();                 // before anyone counts on
+                if (held > kCap) break;
+                if (held > kLimit) {
+                    reduce(held);
+                    // the floor is the least kept logit
+                    uint32_t low = tid < n_out ? (uint32_t)(tmp[tid] >> 32) : 0xffffffffu;
+                    low = __reduce_min_sync(0xffffffffu, low);
+                    if ((tid & 31) == 0) cs.most[tid >> 5] = low;
+                    __syncthreads();
+                    floor = unord(min(cs.most[0], cs.most[1]));      // n_out <= 64: two warps
+                    open = false;
+                    __syncthreads();
+                }
             }
         }
+        __syncthreads();
+        n = count;
+        __syncthreads();
+        if (n <= kCap) break;
+        if (tid == 0) count = 0;
+        m = floor = -INFINITY;
+        sum = 0;
+        open = true;
+        __syncthreads();
     }
-    __syncthreads();
-    int n = count;
-    __syncthreads();
-    if (n > 2 * kMaxOut || n > kThreads) {
+    if (n > 2 * kMaxOut) {
         reduce(n);
         n = n_out;
     }
