@@ -446,7 +446,7 @@ BC_API bc_status bc_lora_add(const void *x, bc_dtype x_dtype, const void *A, con
  *                 overlapping calls must not share it
  * Masked tokens have the logit -inf (NaN counts as -inf, +inf as the largest
  * finite value); candidates of total -inf fill up the list where no others
- * are left.  beams <= 32, batch * beams <= 65535, V < 2^30, beams * V < 2^32.
+ * are left.  beams <= 32, batch * beams <= 65535, V <= 2^22.
  * Totals are formed and compared in fp64; the sums of exponentials carry
  * fp32 exponentials (about 1e-7 relative).
  */

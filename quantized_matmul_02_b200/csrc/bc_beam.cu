@@ -6,17 +6,17 @@
 // ties going to the lowest w * V + v.
 //
 // Two launches.  The first one reads the logits once: a block owns one span of
-// one beam's row, keeps a reference near its maximum, the sum of exponentials, and the
-// span's n_out best (logit, token) -- within a beam the order by total is the
-// order by logit.  After its first tile a logit costs a comparison with the
-// n_out-th best so far.  The second one joins the spans of each beam and
-// selects over a request's beams.  HBM bound: 4 bytes per logit against about
-// seven operations.
+// one beam's row and keeps the sum of exponentials and, for every 16 logits
+// that a thread reads together, their maximum.  The n_out best logits lie in
+// the n_out groups with the best maxima (within a beam the order by total is
+// the order by logit), so only those groups' logits are looked at again.  The
+// second launch joins the spans of each beam and selects over a request's
+// beams.  HBM bound: 4 bytes per logit against about seven operations.
 //
 // Keys (value, place) are all distinct, so the result does not depend on the
 // order in which candidates are collected.
 //
-// Precision: exponentials in fp32 relative to that reference, eight
+// Precision: exponentials in fp32 relative to a value near their maximum, eight
 // added in fp32, the rest in fp64, totals in fp64.  Order between beams is
 // decided on fp64 totals, so two candidates change places only where their
 // totals agree to about 1e-7.
@@ -32,8 +32,8 @@ constexpr int kTile = kThreads * kPer;
 constexpr int64_t kSms = 148;
 constexpr int kMaxOut = 64;
 constexpr int kMaxBeams = 32;
-constexpr int kLimit = kThreads;                 // kept candidates before they are reduced
-constexpr int kCap = kLimit + kTile;
+constexpr int kMaxTiles = 32;                    // per span
+constexpr int64_t kMaxV = 1 << 22;
 constexpr float kMax = 3.402823466e38f;
 
 // Order-preserving map of a float to an unsigned; -inf is kNegInf, and 0 is
@@ -153,7 +153,7 @@ struct SelectArgs {
     const uint8_t *finished;                     // [batch][beams] or null
     int64_t V;
     int beams, n_out, spans;
-    int span;                                    // logits per span, a multiple of kTile
+    int span;                                    // logits per span: up to kMaxTiles of kTile
     int32_t eos, pad;
     SpanOut *heads;                              // [rows][spans]
     uint64_t *keys;                              // [rows][spans][n_out], each list in order
@@ -170,9 +170,10 @@ __device__ __forceinline__ bool idle(const SelectArgs &a, int64_t r) {
 
 // grid: rows x spans.  Places u of a row count from the 16-byte boundary at or
 // before its first logit (token = u - skip), so that any V reads whole words.
-__global__ void __launch_bounds__(kThreads, 3) beam_span_kernel(const SelectArgs a) {
-    __shared__ uint64_t buf[kCap];
-    __shared__ uint64_t tmp[kMaxOut];
+__global__ void __launch_bounds__(kThreads, 4) beam_span_kernel(const SelectArgs a) {
+    __shared__ uint32_t best[kMaxTiles][kThreads];   // ord(maximum) of each group, 0: no logits in it
+    __shared__ uint64_t kept[kMaxOut];
+    __shared__ int picked[kMaxOut];              // groups: tile * kThreads + thread
     __shared__ ChooseShared cs;
     __shared__ double dsh[kWarps];
     __shared__ float fsh[kWarps];
@@ -187,13 +188,12 @@ __global__ void __launch_bounds__(kThreads, 3) beam_span_kernel(const SelectArgs
     row -= skip;                                 // (never read before its first logit)
     const int tid = threadIdx.x, n_out = a.n_out;
     if (tid == 0) count = 0;
-    float m = -INFINITY, floor = -INFINITY;      // logits have to be above the floor ...
-    bool open = true;                            // ... once there is one
+    float m = -INFINITY;
     double sum = 0;
-    auto inside = [&](int t0) { return t0 >= skip && t0 + kTile <= u1; };
-    auto place = [&](int t0, int i) { return t0 + (i / 4 * kThreads + tid) * 4 + (i & 3); };
+    // element i of a thread's group in the tile that begins at t0
+    auto place = [](int t0, int thread, int i) { return t0 + (i / 4 * kThreads + thread) * 4 + (i & 3); };
     auto load = [&](int t0, float (&x)[kPer]) {
-        if (inside(t0)) {
+        if (t0 >= skip && t0 + kTile <= u1) {
             const float4 *p = reinterpret_cast<const float4 *>(row + t0) + tid;
 #pragma unroll
             for (int i = 0; i < kPer; i += 4) {
@@ -206,155 +206,135 @@ __global__ void __launch_bounds__(kThreads, 3) beam_span_kernel(const SelectArgs
         } else {
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const int u = place(t0, i);
+                const int u = place(t0, tid, i);
                 x[i] = u >= skip && u < u1 ? __ldcs(row + u) : -INFINITY;
             }
         }
     };
-    // The n_out largest of buf's keys (more than n_out) move to its front, in no order.
-    auto reduce = [&](int held) {
-        auto move = [&](auto &k) {
-            constexpr int P = sizeof(k) / sizeof(k[0]);
+    float next[kPer];
+    load(u0, next);
+    int tiles = 0;
+    for (int t0 = u0; t0 < u1; t0 += kTile, ++tiles) {
+        float x[kPer];
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int at = i * kThreads + tid;
-                const uint64_t key = at < held ? buf[at] : 0;
-                k[i][0] = (uint32_t)(key >> 32);
-                k[i][1] = (uint32_t)key;
+        for (int i = 0; i < kPer; ++i) x[i] = next[i];
+        if (t0 + kTile < u1) load(t0 + kTile, next);
+        float total = x[0], top;
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) total += x[i];
+        if (!(total < INFINITY))                 // a NaN or +inf among them, or very large ones
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) x[i] = sane(x[i]);
+        top = x[0];
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
+        uint32_t key = ord(top);
+        if (top > -INFINITY) {
+            // the reference follows a larger maximum only when it has to: sums of
+            // values up to exp(16) are as exact, and a change costs an fp64 exponential
+            if (top > m + 16.f || m == -INFINITY) {
+                sum *= exp((double)m - (double)top);
+                m = top;
             }
-            const uint32_t mine = choose(k, n_out, cs);
-            if (tid == 0) count = 0;
-            __syncthreads();
+            float s[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-                if (mine >> i & 1) tmp[atomicAdd(&count, 1)] = (uint64_t)k[i][0] << 32 | k[i][1];
-        };
-        if (held <= kThreads) {
-            uint32_t k[1][2];
-            move(k);
-        } else {
-            uint32_t k[(kCap + kThreads - 1) / kThreads][2];
-            move(k);
+            for (int i = 0; i < kPer; ++i) s[i & 1] += exp2_fast((x[i] - m) * kLog2e);
+            sum += (double)s[0] + (double)s[1];
+        } else if (!(t0 >= skip && t0 + kTile <= u1)) {
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) any |= place(t0, tid, i) >= skip && place(t0, tid, i) < u1;
+            if (!any) key = 0;
         }
+        best[tiles][tid] = key;
+    }
+    __syncthreads();
+
+    // the best groups: more than one thread's worth of any tile only by chance
+    auto logit = [&](int group, int i, int &u) {
+        u = place(u0 + group / kThreads * kTile, group % kThreads, i);
+        return u >= skip && u < u1 ? sane(row[u]) : -INFINITY;
+    };
+    auto pick = [&](auto &k) {
+        constexpr int P = sizeof(k) / sizeof(k[0]);
+#pragma unroll
+        for (int i = 0; i < P; ++i) k[i][0] = i < tiles ? best[i][tid] : 0;
+        const uint32_t mine = choose(k, n_out, cs);
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (mine >> i & 1) picked[atomicAdd(&count, 1)] = i * kThreads + tid;
         __syncthreads();
-        if (tid < n_out) buf[tid] = tmp[tid];
+        const int got = count;
+        if (got == n_out) return;
+        // Fewer: all groups, or all but some of equal maxima, of which those with
+        // the lowest places are wanted.  A group's is its first logit of that value.
+        uint32_t rest = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (!(mine >> i & 1)) rest = max(rest, k[i][0]);
+        rest = __reduce_max_sync(0xffffffffu, rest);
+        if ((tid & 31) == 0) cs.most[tid >> 5] = rest;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) rest = max(rest, cs.most[i]);
+        if (rest == 0) return;
+        uint32_t k2[P][1];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            k2[i][0] = 0;
+            if (!(mine >> i & 1) && k[i][0] == rest)
+                for (int e = kPer - 1; e >= 0; --e) {
+                    int u;
+                    const float f = logit(i * kThreads + tid, e, u);
+                    if (u >= skip && u < u1 && ord(f) == rest) k2[i][0] = ~(uint32_t)(u - skip);
+                }
+        }
+        const uint32_t more = choose(k2, n_out - got, cs);
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (more >> i & 1) picked[atomicAdd(&count, 1)] = i * kThreads + tid;
         __syncthreads();
     };
-    // Candidates are collected without waiting for one another, as far as buf
-    // goes; every `every` tiles they are reduced.  Logits that rise along the
-    // row can bring more: then the span is read again, with room for all of a
-    // tile before each.
-    int n = 0;
-    for (int every = 4;; every = 1) {
-        float next[kPer];
-        load(u0, next);
-        int tile = 0;
-        for (int t0 = u0; t0 < u1; t0 += kTile, ++tile) {
-            float x[kPer];
+    if (tiles == 1) {
+        uint32_t k[1][1];
+        pick(k);
+    } else if (tiles <= 8) {
+        uint32_t k[8][1];
+        pick(k);
+    } else {
+        uint32_t k[kMaxTiles][1];
+        pick(k);
+    }
+    const int cands = count * kPer;
+    __syncthreads();
+    if (tid == 0) count = 0;
+    // the best logits of those groups
+    auto keep = [&](auto &k) {
+        constexpr int P = sizeof(k) / sizeof(k[0]);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) x[i] = next[i];
-            if (t0 + kTile < u1) load(t0 + kTile, next);
-            float total = x[0], tops[kPer / 4];
-#pragma unroll
-            for (int i = 1; i < kPer; ++i) total += x[i];
-            if (!(total < INFINITY))             // a NaN or +inf among them, or very large ones
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) x[i] = sane(x[i]);
-#pragma unroll
-            for (int i = 0; i < kPer / 4; ++i)
-                tops[i] = fmaxf(fmaxf(x[4 * i], x[4 * i + 1]), fmaxf(x[4 * i + 2], x[4 * i + 3]));
-            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-            if (top > -INFINITY) {
-                // the reference follows a larger maximum only when it has to: sums of
-                // values up to exp(16) are as exact, and a change costs an fp64 exponential
-                if (top > m + 16.f || m == -INFINITY) {
-                    sum *= exp((double)m - (double)top);
-                    m = top;
-                }
-                float s[2] = {0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) s[i & 1] += exp2_fast((x[i] - m) * kLog2e);
-                sum += (double)s[0] + (double)s[1];
-            }
-            const bool first = tile == 0;
-            if (first) {
-                // the n_out-th largest of the threads' best logits: n_out of them reach it
-                bool any = false;
-#pragma unroll
-                for (int i = 0; i < kPer; i += 3) any |= place(t0, i) >= skip && place(t0, i) < u1;
-                const uint32_t k[1][1] = {{any ? ord(top) : 0}};
-                const uint32_t mine = choose(k, n_out, cs);
-                if (__syncthreads_count(k[0][0] != 0) >= n_out) {
-                    // (equal logits may leave `mine` short of n_out: then all that equal the rest are wanted)
-                    const int got = __syncthreads_count(mine);
-                    uint32_t low = got == n_out ? (mine ? k[0][0] : 0xffffffffu)
-                                                : (mine || k[0][0] == 0 ? 0 : k[0][0]);
-                    low = got == n_out ? __reduce_min_sync(0xffffffffu, low) : __reduce_max_sync(0xffffffffu, low);
-                    if ((tid & 31) == 0) cs.most[tid >> 5] = low;
-                    __syncthreads();
-#pragma unroll
-                    for (int i = 0; i < kWarps; ++i)
-                        low = got == n_out ? min(low, cs.most[i]) : max(low, cs.most[i]);
-                    floor = unord(low);
-                    open = false;
-                }
-            }
-            // candidates reach the floor (first tile), or are above it: later equals lose
-            auto wanted = [&](float f) { return first ? f >= floor : open || f > floor; };
-            if (wanted(top)) {
-                const bool all = inside(t0);
-#pragma unroll
-                for (int q = 0; q < kPer / 4; ++q)
-                    if (wanted(tops[q]))
-#pragma unroll
-                        for (int i = q * 4; i < q * 4 + 4; ++i)
-                            if (wanted(x[i])) {
-                                const int u = place(t0, i);
-                                if (all || (u >= skip && u < u1)) {
-                                    const int to = atomicAdd(&count, 1);
-                                    if (to < kCap) buf[to] = (uint64_t)ord(x[i]) << 32 | (uint32_t)~(uint32_t)(u - skip);
-                                }
-                            }
-            }
-            if (tile % every == every - 1) {
-                __syncthreads();
-                const int held = count;
-                __syncthreads();                 // before anyone counts on
-                if (held > kCap) break;
-                if (held > kLimit) {
-                    reduce(held);
-                    // the floor is the least kept logit
-                    uint32_t low = tid < n_out ? (uint32_t)(tmp[tid] >> 32) : 0xffffffffu;
-                    low = __reduce_min_sync(0xffffffffu, low);
-                    if ((tid & 31) == 0) cs.most[tid >> 5] = low;
-                    __syncthreads();
-                    floor = unord(min(cs.most[0], cs.most[1]));      // n_out <= 64: two warps
-                    open = false;
-                    __syncthreads();
+        for (int i = 0; i < P; ++i) {
+            const int c = i * kThreads + tid;
+            k[i][0] = k[i][1] = 0;
+            if (c < cands) {
+                int u;
+                const float f = logit(picked[c / kPer], c % kPer, u);
+                if (u >= skip && u < u1) {
+                    k[i][0] = ord(f);
+                    k[i][1] = ~(uint32_t)(u - skip);
                 }
             }
         }
-        __syncthreads();
-        n = count;
-        __syncthreads();
-        if (n <= kCap) break;
-        if (tid == 0) count = 0;
-        m = floor = -INFINITY;
-        sum = 0;
-        open = true;
-        __syncthreads();
-    }
-    if (n > 2 * kMaxOut) {
-        reduce(n);
-        n = n_out;
-    }
-    // in order: a key's rank is its place
-    const int64_t at = r * a.spans + sp;
-    if (tid < n) {
-        const uint64_t k = buf[tid];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += buf[j] > k;
-        if (rank < n_out) a.keys[at * n_out + rank] = k;
+        const uint32_t mine = choose(k, n_out, cs);
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (mine >> i & 1) kept[atomicAdd(&count, 1)] = (uint64_t)k[i][0] << 32 | k[i][1];
+    };
+    if (cands <= kThreads) {
+        uint32_t k[1][2];
+        keep(k);
+    } else {
+        uint32_t k[kMaxOut * kPer / kThreads][2];
+        keep(k);
     }
     // one reference and sum for the span
     float bm = m;
@@ -369,11 +349,19 @@ __global__ void __launch_bounds__(kThreads, 3) beam_span_kernel(const SelectArgs
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if ((tid & 31) == 0) dsh[tid >> 5] = s;
     __syncthreads();
+    // in order: a key's rank is its place
+    const int64_t at = r * a.spans + sp;
+    const int n = count;
+    if (tid < n) {
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += kept[j] > kept[tid];
+        a.keys[at * n_out + rank] = kept[tid];
+    }
     if (tid == 0) {
         s = 0;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) s += dsh[i];
-        a.heads[at] = SpanOut{s, bm, min(n, n_out)};
+        a.heads[at] = SpanOut{s, bm, n};
     }
 }
 
@@ -397,7 +385,8 @@ __device__ __forceinline__ uint32_t choose(const Key (&k)[P], int n, ChooseShare
     return choose(w, n, sh);
 }
 
-constexpr int kMaxLists = 6 * kThreads;          // a request's spans: at most 8 * kSms + kMaxBeams
+constexpr int kMaxLists = 6 * kThreads;          // a request's spans: at most 8 * kSms + kMaxBeams, or
+                                                 // kMaxBeams * (kMaxV / (kMaxTiles * kTile) + 1)
 
 // one block per request
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const SelectArgs a) {
@@ -544,7 +533,8 @@ int spans_of(int64_t rows, int64_t V) {
     int64_t want = (8 * kSms + rows - 1) / rows;
     if (want > tiles) want = tiles;
     if (want < 1) want = 1;
-    const int64_t per = (tiles + want - 1) / want;
+    int64_t per = (tiles + want - 1) / want;
+    if (per > kMaxTiles) per = kMaxTiles;
     return (int)((tiles + per - 1) / per);
 }
 
@@ -555,10 +545,9 @@ bool overlap(const void *p, size_t pn, const void *q, size_t qn) {
 
 bc_status check_sizes(int64_t batch, int64_t beams, int64_t V, int64_t n_out) {
     if (batch <= 0 || beams <= 0 || V <= 0 || n_out <= 0) return BC_ERR_INVALID_ARG;
-    if (beams > kMaxBeams || n_out > kMaxOut || V >= (int64_t)1 << 30 || batch * beams > 65535 ||
+    if (beams > kMaxBeams || n_out > kMaxOut || V > kMaxV || batch * beams > 65535 ||
         batch > 65535)
         return BC_ERR_UNSUPPORTED;
-    if (beams * V >= (int64_t)1 << 32) return BC_ERR_UNSUPPORTED;
     if (n_out > beams * V) return BC_ERR_INVALID_ARG;
     return BC_OK;
 }

@@ -206,8 +206,8 @@ def test_select_rejects_on_host():
         assert call(**{k: None}) == 1
     for k in ("batch", "beams", "V", "n_out"):
         assert call(**{k: 0}) == 1 and call(**{k: -3}) == 1
-    assert call(beams=33) == 2 and call(n_out=65) == 2 and call(V=1 << 30) == 2 and call(batch=1 << 16) == 2
-    assert call(beams=4, V=(1 << 30) - 1, wsb=256) == 4 and call(beams=5, V=(1 << 30) - 1) == 2
+    assert call(beams=33) == 2 and call(n_out=65) == 2 and call(V=(1 << 22) + 1) == 2 and call(batch=1 << 16) == 2
+    assert call(V=1 << 22, wsb=256) == 4
     assert call(V=1, n_out=5) == 1                   # fewer continuations than asked for
     assert call(finished=at[2], pad=1000) == 1 and call(finished=at[2], pad=-1) == 1
     assert call(logits=at[0] + 2) == 3 and call(ws=at[6] + 16) == 3
