@@ -173,7 +173,7 @@ __device__ __forceinline__ bool idle(const SelectArgs &a, int64_t r) {
 __global__ void __launch_bounds__(kThreads, 4) beam_span_kernel(const SelectArgs a) {
     __shared__ uint32_t best[kMaxTiles][kThreads];   // ord(maximum) of each group, 0: no logits in it
     __shared__ uint64_t kept[kMaxOut];
-    __shared__ int picked[kMaxOut];              // groups: tile * kThreads + thread
+    __shared__ int picked[kMaxOut], list[kThreads];  // groups: tile * kThreads + thread
     __shared__ ChooseShared cs;
     __shared__ double dsh[kWarps];
     __shared__ float fsh[kWarps];
@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_span_kernel(const SelectArgs
     float next[kPer];
     load(u0, next);
     int tiles = 0;
+    uint32_t own = 0;                            // the best of this thread's groups
     for (int t0 = u0; t0 < u1; t0 += kTile, ++tiles) {
         float x[kPer];
 #pragma unroll
@@ -247,22 +248,23 @@ __global__ void __launch_bounds__(kThreads, 4) beam_span_kernel(const SelectArgs
             if (!any) key = 0;
         }
         best[tiles][tid] = key;
+        own = max(own, key);
     }
     __syncthreads();
 
-    // the best groups: more than one thread's worth of any tile only by chance
+    // The best groups.  n_out threads' own best reach `bar`, so no group below
+    // it is among them; those that reach it are few, but for equal logits.
     auto logit = [&](int group, int i, int &u) {
         u = place(u0 + group / kThreads * kTile, group % kThreads, i);
         return u >= skip && u < u1 ? sane(row[u]) : -INFINITY;
     };
-    auto pick = [&](auto &k) {
+    // k: maxima of groups, group(i) this thread's i-th
+    auto pick = [&](auto &k, auto group) {
         constexpr int P = sizeof(k) / sizeof(k[0]);
-#pragma unroll
-        for (int i = 0; i < P; ++i) k[i][0] = i < tiles ? best[i][tid] : 0;
         const uint32_t mine = choose(k, n_out, cs);
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            if (mine >> i & 1) picked[atomicAdd(&count, 1)] = i * kThreads + tid;
+            if (mine >> i & 1) picked[atomicAdd(&count, 1)] = group(i);
         __syncthreads();
         const int got = count;
         if (got == n_out) return;
@@ -285,25 +287,55 @@ __global__ void __launch_bounds__(kThreads, 4) beam_span_kernel(const SelectArgs
             if (!(mine >> i & 1) && k[i][0] == rest)
                 for (int e = kPer - 1; e >= 0; --e) {
                     int u;
-                    const float f = logit(i * kThreads + tid, e, u);
+                    const float f = logit(group(i), e, u);
                     if (u >= skip && u < u1 && ord(f) == rest) k2[i][0] = ~(uint32_t)(u - skip);
                 }
         }
         const uint32_t more = choose(k2, n_out - got, cs);
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            if (more >> i & 1) picked[atomicAdd(&count, 1)] = i * kThreads + tid;
+            if (more >> i & 1) picked[atomicAdd(&count, 1)] = group(i);
         __syncthreads();
     };
-    if (tiles == 1) {
-        uint32_t k[1][1];
-        pick(k);
+    uint32_t bar = 1;
+    {
+        const uint32_t k[1][1] = {{own}};
+        const uint32_t mine = choose(k, n_out, cs);
+        const int got = __syncthreads_count(mine), all = __syncthreads_count(own != 0);
+        if (all > n_out) {
+            // the least of the chosen, or, where equal ones were left, their value
+            bar = got == n_out ? __reduce_min_sync(0xffffffffu, mine ? own : 0xffffffffu)
+                               : __reduce_max_sync(0xffffffffu, mine ? 0 : own);
+            if ((tid & 31) == 0) cs.most[tid >> 5] = bar;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) bar = got == n_out ? min(bar, cs.most[i]) : max(bar, cs.most[i]);
+        }
+    }
+    for (int i = 0; own >= bar && i < tiles; ++i)
+        if (best[i][tid] >= bar) {
+            const int to = atomicAdd(&count, 1);
+            if (to < kThreads) list[to] = i * kThreads + tid;
+        }
+    __syncthreads();
+    const int listed = count;
+    __syncthreads();
+    if (tid == 0) count = 0;
+    auto each = [&](int i) { return i * kThreads + tid; };
+    if (listed <= kThreads) {
+        const int mine = tid < listed ? list[tid] : 0;
+        uint32_t k[1][1] = {{tid < listed ? best[mine / kThreads][mine % kThreads] : 0}};
+        pick(k, [&](int) { return mine; });
     } else if (tiles <= 8) {
         uint32_t k[8][1];
-        pick(k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k[i][0] = i < tiles ? best[i][tid] : 0;
+        pick(k, each);
     } else {
         uint32_t k[kMaxTiles][1];
-        pick(k);
+#pragma unroll
+        for (int i = 0; i < kMaxTiles; ++i) k[i][0] = i < tiles ? best[i][tid] : 0;
+        pick(k, each);
     }
     const int cands = count * kPer;
     __syncthreads();
@@ -385,7 +417,7 @@ __device__ __forceinline__ uint32_t choose(const Key (&k)[P], int n, ChooseShare
     return choose(w, n, sh);
 }
 
-constexpr int kMaxLists = 6 * kThreads;          // a request's spans: at most 8 * kSms + kMaxBeams, or
+constexpr int kMaxLists = 6 * kThreads;          // a request's spans: at most 4 * kSms + kMaxBeams, or
                                                  // kMaxBeams * (kMaxV / (kMaxTiles * kTile) + 1)
 
 // one block per request
@@ -526,11 +558,11 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const SelectArgs a)
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Spans per row: enough blocks to fill the GPU several times over, none
-// shorter than one tile.
+// Spans per row: as many blocks as the GPU holds at once (four per SM), none
+// shorter than one tile; each costs its selection at the end.
 int spans_of(int64_t rows, int64_t V) {
     const int64_t tiles = (V + 3 + kTile - 1) / kTile;
-    int64_t want = (8 * kSms + rows - 1) / rows;
+    int64_t want = 4 * kSms / rows;
     if (want > tiles) want = tiles;
     if (want < 1) want = 1;
     int64_t per = (tiles + want - 1) / want;
