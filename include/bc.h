@@ -380,7 +380,7 @@ typedef struct bc_lora_desc {
 
 /*
  * bc_lora_add_batched -- low-rank adapters of many requests at once, added to
- * the outputs of shared projections (bc_matmul_q's y), two launches per 32
+ * the outputs of shared projections (bc_matmul_q's y), two launches per 16
  * projections: for the rows m of segment i, a = seg_adapter[i],
  *   y[m] += scaling[a] * B[a] (A[a] x[m])
  * over the first ranks[a] ranks of R.  Rows of no segment, and rows whose

@@ -364,15 +364,17 @@ def _one_device(what: str, first: torch.Tensor, *tensors: Optional[torch.Tensor]
     dev = first.get_device()
     if dev < 0:
         raise ValueError(f"{what}: expected CUDA tensors")
-    if not first.is_contiguous():
-        raise ValueError(f"{what}: expected contiguous tensors")
+    _same_device(what, dev, first, *tensors)
+    return dev
+
+
+def _same_device(what: str, dev: int, *tensors: Optional[torch.Tensor]) -> None:
     for t in tensors:
         if t is not None:
             if t.get_device() != dev:
                 raise ValueError(f"{what}: all tensors must be on one CUDA device")
             if not t.is_contiguous():
                 raise ValueError(f"{what}: expected contiguous tensors")
-    return dev
 
 
 def _bad(what: str, name: str, t: torch.Tensor, shape, *dtypes) -> None:
@@ -495,19 +497,25 @@ def make_lora_descs(items: Sequence[tuple]) -> LoraDescs:
         raise ValueError(f"{what}: x must be float32 or bfloat16, adapters float16 or bfloat16")
     M, (n, R, _) = x0.shape[0], A0.shape
     dev = x0.get_device()
-    fields = []
+    if dev < 0:
+        raise ValueError(f"{what}: expected CUDA tensors")
+    fields, seen = [], None
     for x, A, B, y in items:
-        _one_device(what, x0, x, A, B, y)
-        K, N = x.shape[-1], y.shape[-1]
-        if x.dtype != xt or x.shape != (M, K):
-            _bad(what, "x", x, (M, K), xt)
+        if x is not seen:                                   # projections in a row share their x
+            K = x.shape[-1]
+            if x.dtype != xt or x.shape != (M, K):
+                _bad(what, "x", x, (M, K), xt)
+            _same_device(what, dev, x)
+            xp, seen = x.data_ptr(), x
+        N = y.shape[-1]
         if A.dtype != wt or A.shape != (n, R, K):
             _bad(what, "A", A, (n, R, K), wt)
         if B.dtype != wt or B.shape != (n, N, R):
             _bad(what, "B", B, (n, N, R), wt)
         if y.dtype != _F32 or y.shape != (M, N):
             _bad(what, "y", y, (M, N), _F32)
-        fields += (x.data_ptr(), A.data_ptr(), B.data_ptr(), y.data_ptr(), N, K)
+        _same_device(what, dev, A, B, y)
+        fields += (xp, A.data_ptr(), B.data_ptr(), y.data_ptr(), N, K)
     d = LoraDescs()
     d.M, d.n_adapters, d.R, d.count, d.device = M, n, R, len(items), dev
     d.x_dtype, d.w_dtype, d.tensors = _DT[xt], _DT[wt], items

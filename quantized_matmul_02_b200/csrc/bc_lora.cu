@@ -36,7 +36,7 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int64_t kSms = 148;
-constexpr int kMaxDescs = 32;          // per launch (kernel parameters)
+constexpr int kMaxDescs = 16;          // per launch (kernel parameters)
 constexpr int kMaxSegments = 4096;
 constexpr int kMaxRank = 128;
 constexpr int kGroupRows = 256;        // up to here rows are ordered by adapter
@@ -646,13 +646,14 @@ bc_status launch(const LoraArgs &a, cudaStream_t s) {
     at[0].val.clusterDim.x = a.split;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.split > 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, shrink_kernel<X, W, MB>, a);
     if (e == cudaSuccess) {
         // expand's blocks may start while shrink's finish; they wait for all of it before they read
         cfg.gridDim = dim3((unsigned)(a.max_tiles * MB * a.col_blocks));
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 1;
         e = cudaLaunchKernelEx(&cfg, expand_kernel<W, MB>, a);
     }
     if (e != cudaSuccess) {
@@ -780,11 +781,10 @@ bc_status bc_lora_add_batched(const bc_lora_desc *descs, int count, int64_t M, i
             a.d[j].group_size = n;
             a.chunks += (n * a.R + kChunk - 1) / kChunk;
         }
-        // parts of K: enough blocks to fill the GPU about three times, with a
-        // step of 32 for every warp
+        // parts of K: about two blocks per SM, each with 1024 of K or more (a
+        // part costs two cluster barriers, about 1.5 us)
         a.split = 1;
-        while (a.split < kMaxSplit && (int64_t)a.max_tiles * a.chunks * a.split < 3 * kSms &&
-               a.split * 2 * kWarps <= (K / 32 + kWarps - 1) / kWarps * kWarps)
+        while (a.split < kMaxSplit && (int64_t)a.max_tiles * a.chunks * a.split < 2 * kSms && K / a.split >= 1024)
             a.split *= 2;
         if (x_dtype == BC_F32)
             st = w_dtype == BC_F16 ? launch<float, __half>(a, s) : launch<float, __nv_bfloat16>(a, s);
