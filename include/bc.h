@@ -411,8 +411,8 @@ BC_API bc_status bc_lora_add_batched(const bc_lora_desc *descs, int count, int64
                                      void *workspace, size_t workspace_bytes,
                                      bc_stream_t stream);
 
-/* Workspace bytes bc_lora_add_batched needs (reads N and K of each descriptor;
- * 0 if the sizes would be rejected). */
+/* Workspace bytes bc_lora_add_batched needs (reads x, N and K of each
+ * descriptor; 0 if the sizes would be rejected). */
 BC_API size_t bc_workspace_size_lora(const bc_lora_desc *descs, int count, int64_t M,
                                      int64_t R, int64_t n_adapters, int64_t n_segments,
                                      bc_dtype x_dtype);

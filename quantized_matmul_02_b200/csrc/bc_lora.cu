@@ -5,11 +5,10 @@
 //   ranks of R in use.
 //
 // Two launches for a whole set of projections.  Rows that share an adapter
-// are cut into tiles.  shrink_kernel forms c A x, a cluster per (tile, 32 ranks
-// of the projections that read the same x), its blocks sharing K and joining
-// their sums through distributed shared memory; it leaves them in scratch, in
-// the order of expand_kernel's fragments.  expand_kernel adds B v, a block per
-// (16 rows, 256 columns).  x, A, B, v and y go between global memory and
+// are cut into tiles.  shrink_kernel forms c A x, a block per (tile, 32 ranks of
+// the projections that read the same x, part of K), and leaves it in scratch,
+// in the order of expand_kernel's fragments.  expand_kernel joins the parts
+// and adds B v, a block per (16 rows, columns).  x, A, B, v and y go between global memory and
 // matrix fragments directly: the order of the contraction index is free, so a
 // lane takes 16-byte pieces along it, and y's columns are dealt to the
 // fragments so that lanes side by side hold whole sectors.
@@ -24,14 +23,11 @@
 // Sums run in a fixed order: results do not change from call to call.
 #include "bc_internal.cuh"
 
-#include <cooperative_groups.h>
-
+#include <mutex>
 #include <type_traits>
 
 namespace bc {
 namespace {
-
-namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -42,10 +38,11 @@ constexpr int kMaxRank = 128;
 constexpr int kGroupRows = 256;        // up to here rows are ordered by adapter
 constexpr int kChunk = 32;             // ranks per shrink block
 constexpr int kFew = 2;                // rows up to here: plain products instead of fragments
-constexpr int kMaxSplit = 8;           // parts of K (blocks of a cluster)
+constexpr int kMaxSplit = 8;           // parts of K
 constexpr int kStep = kWarps * 32;     // columns an expand block takes at a time
 constexpr int kMaxSteps = 12;          // such steps per block
 constexpr int kStages = 3;             // of which y is on its way
+constexpr int kRing = kWarps * kStages * 4 * 32;   // 16-byte pieces of y in shared memory
 
 struct Desc {
     const void *x, *A, *B;
@@ -55,8 +52,9 @@ struct Desc {
     int first_block, blocks;           // expand: this projection's column blocks
 };
 // A tile: `rows` rows of `adapter`.  Row i is first + i, or order[first + i].
-struct Tile {
-    int first, rows, adapter, unused;
+struct __align__(16) Tile {
+    int first, rows, adapter, rank;
+    float scale;
 };
 struct LoraArgs {
     Desc d[kMaxDescs];
@@ -72,7 +70,7 @@ struct LoraArgs {
     int chunks;                        // 32-rank chunks of all groups
     int *head;                         // scratch: the rows' order (grouped)
     Tile *tiles;                       // scratch: [max_tiles], rows = 0 where unused
-    float4 *v;                         // scratch: [count][max_tiles][MB][R16 / 16][2][32]
+    float4 *v;                         // scratch: [count][split][max_tiles][MB][R16 / 16][2][32]
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -122,7 +120,10 @@ __device__ __forceinline__ void segment(const LoraArgs &a, int i, int &s0, int &
     s1 = (int)min((int64_t)max(a.seg_start[i + 1], s0), a.M);
 }
 __device__ __forceinline__ bool usable(const LoraArgs &a, int ad) {
-    return ad >= 0 && ad < a.adapters && (!a.ranks || a.ranks[ad] > 0);
+    return ad >= 0 && ad < a.adapters;
+}
+__device__ __forceinline__ Tile tile_of(const LoraArgs &a, int first, int rows, int ad) {
+    return Tile{first, rows, ad, a.ranks ? min(max(a.ranks[ad], 0), a.R) : a.R, a.scaling ? a.scaling[ad] : 1.f};
 }
 template <int T>
 __device__ __forceinline__ void plan(const LoraArgs &a, PlanShared &p, int want, bool publish) {
@@ -135,18 +136,18 @@ __device__ __forceinline__ void plan(const LoraArgs &a, PlanShared &p, int want,
         __syncthreads();
         for (int i = tid; i < a.S; i += kThreads) {
             int s0, s1;
+            const int ad = a.seg_adapter[i];
             segment(a, i, s0, s1);
-            if (s0 < s1) {
-                const int ad = a.seg_adapter[i];
-                if (usable(a, ad))
-                    for (int m = s0; m < s1; ++m) p.key[m] = ad;
-            }
+            if (usable(a, ad))
+                for (int m = s0; m < s1; ++m) p.key[m] = ad;
         }
         __syncthreads();
         // a row's place: how many keys come before it.  Threads lie idle where
         // rows are few, so up to eight of them share a row.
         const int share = M <= 32 ? 8 : M <= 64 ? 4 : M <= 128 ? 2 : 1;
         const int who = tid / share, mine = p.key[who];
+        Tile t{};
+        if (mine != kNone) t = tile_of(a, 0, 0, mine);       // (on its way while rows are counted)
         int before = 0, same = 0, all = 0;
         for (int j = tid % share * 4; j < M; j += share * 4) {       // places behind M hold kNone
             const int4 q = *reinterpret_cast<const int4 *>(p.key + j);
@@ -184,8 +185,9 @@ __device__ __forceinline__ void plan(const LoraArgs &a, PlanShared &p, int want,
         __syncthreads();
         if (head) {
             const int n = p.key[tid];
-            const Tile t{before, min(T, all - same), mine, 0};
             if (n == want) {
+                t.first = before;
+                t.rows = min(T, all - same);
                 p.mine = t;
                 p.found = 1;
             }
@@ -199,8 +201,9 @@ __device__ __forceinline__ void plan(const LoraArgs &a, PlanShared &p, int want,
     const int per = (a.S + kThreads - 1) / kThreads;
     const int i0 = min(a.S, tid * per), i1 = min(a.S, i0 + per);
     auto tiles_in = [&](int i, int &s0, int &s1) {
+        const int ad = a.seg_adapter[i];
         segment(a, i, s0, s1);
-        return s0 < s1 && usable(a, a.seg_adapter[i]) ? (s1 - s0 + T - 1) / T : 0;
+        return usable(a, ad) ? (s1 - s0 + T - 1) / T : 0;
     };
     int own = 0, s0, s1;
     for (int i = i0; i < i1; ++i) own += tiles_in(i, s0, s1);
@@ -218,7 +221,7 @@ __device__ __forceinline__ void plan(const LoraArgs &a, PlanShared &p, int want,
         const int n = tiles_in(i, s0, s1);
         if (want >= at && want < at + n) {
             const int f = s0 + (want - at) * T;
-            p.mine = Tile{f, min(T, s1 - f), a.seg_adapter[i], 0};
+            p.mine = tile_of(a, f, min(T, s1 - f), a.seg_adapter[i]);
             p.found = 1;
         }
         at += n;
@@ -226,7 +229,7 @@ __device__ __forceinline__ void plan(const LoraArgs &a, PlanShared &p, int want,
     __syncthreads();
 }
 
-// grid: tiles x rank chunks x parts of K; a cluster is the parts of one K
+// grid: tiles x rank chunks x parts of K
 template <typename X, typename W, int MB>
 __global__ void __launch_bounds__(kThreads, 2)
 shrink_kernel(const __grid_constant__ LoraArgs a) {
@@ -243,9 +246,9 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
     int chunk = inner / a.split;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     plan<T>(a, ps, ti, blockIdx.x == 0);
-    const Tile tile = ps.found ? ps.mine : Tile{0, 0, 0, 0};
+    const Tile tile = ps.found ? ps.mine : Tile{};
     if (inner == 0 && tid == 0) a.tiles[ti] = tile;
-    if (!ps.found) return;                                     // (the whole cluster)
+    if (!ps.found) return;
     // the chunk's projections: blocks of eight ranks of all that read one x, in a row
     const int R = a.R, R8 = R / 8, R16 = (R + 15) / 16 * 16, n_rows = tile.rows;
     int first = 0;
@@ -254,15 +257,14 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
         first += a.d[first].group_size;
     }
     const int K = a.d[first].K, blocks = a.d[first].group_size * R8;
-    const int rank = a.ranks ? min(a.ranks[tile.adapter], R) : R, used = (rank + 7) / 8;
-    const float scale = a.scaling ? a.scaling[tile.adapter] : 1.f;
+    const int rank = tile.rank, used = (rank + 7) / 8;
     unsigned live = 0;                                         // blocks that have ranks
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const int vb = chunk * NB + b;
         if (vb < blocks && vb % R8 < used) live |= 1u << b;
     }
-    if (!live) return;                                         // (the whole cluster)
+    if (!live) return;
     // row g of block b of A, or null
     auto a_row = [&](int b, int g) -> const W * {
         const int vb = chunk * NB + b, r = vb % R8 * 8 + g;
@@ -460,33 +462,19 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
             red[i] = s;
         }
     }
-    // the cluster's sum: every block takes a share of the places
-    cg::cluster_group cluster = cg::this_cluster();
-    if (a.split > 1) cluster.sync();
-    else __syncthreads();
-    for (int i = part * kThreads + tid; i < kQuads; i += a.split * kThreads) {
+    // to scratch: ranks rb * 8 + 2 t and the next, of rows g and g + 8, are half
+    // of a lane's four ranks there
+    __syncthreads();
+    for (int i = tid; i < kQuads; i += kThreads) {
         const int mb = i / 32 / NB, vb = chunk * NB + i / 32 % NB, rb = vb % R8;
         if (vb >= blocks || rb >= used || mb * 16 >= n_rows) continue;
-        float4 s = red[i];
-        if (a.split > 1) {
-            s = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = 0; c < a.split; ++c) {
-                const float4 p = cluster.map_shared_rank(red, c)[i];
-                s.x += p.x;
-                s.y += p.y;
-                s.z += p.z;
-                s.w += p.w;
-            }
-        }
-        // ranks rb * 8 + 2 t and the next, of rows g and g + 8: half of a lane's four ranks there
+        const float4 s = red[i];
         const int l = i & 31, q = rb / 2, lq = (rb & 1) * 2 + (l & 3) / 2;
-        float2 *out = reinterpret_cast<float2 *>(
-            a.v + ((((int64_t)(first + vb / R8) * a.max_tiles + ti) * MB + mb) * (R16 / 16) + q) * 64 +
-            (l >> 2) * 4 + lq) + (l & 1);
-        out[0] = make_float2(s.x * scale, s.y * scale);
-        out[64] = make_float2(s.z * scale, s.w * scale);
+        const int64_t at = ((int64_t)(first + vb / R8) * a.split + part) * a.max_tiles + ti;
+        float2 *out = reinterpret_cast<float2 *>(a.v + ((at * MB + mb) * (R16 / 16) + q) * 64 + (l >> 2) * 4 + lq) + (l & 1);
+        out[0] = make_float2(s.x * tile.scale, s.y * tile.scale);
+        out[64] = make_float2(s.z * tile.scale, s.w * tile.scale);
     }
-    if (a.split > 1) cluster.sync();                           // the others may still read this block's sums
 }
 
 __device__ __forceinline__ void copy16(float4 *to, const float *from) {
@@ -498,8 +486,8 @@ __device__ __forceinline__ void copy16(float4 *to, const float *from) {
 template <typename W, int MB>
 __global__ void __launch_bounds__(kThreads, 3)
 expand_kernel(const __grid_constant__ LoraArgs a) {
-    // each lane's own pieces of y, loaded two steps ahead: only their owner touches them
-    __shared__ __align__(16) float4 ring[kWarps][kStages][4][32];
+    extern __shared__ __align__(16) float4 smem[];
+    float4 *const vs = smem + kRing;                           // v of the 16 rows: [R16 / 16][2][32]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int sub = blockIdx.x / a.col_blocks, cb = blockIdx.x - sub * a.col_blocks;
     const int ti = sub / MB, mb = sub - ti * MB;
@@ -509,7 +497,7 @@ expand_kernel(const __grid_constant__ LoraArgs a) {
     const int N = d.N, R = a.R, R16 = (R + 15) / 16 * 16;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Tile tile = a.tiles[ti];
-    if (mb * 16 >= tile.rows) return;
+    if (mb * 16 >= tile.rows || tile.rank == 0) return;
     float *yrow[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -524,6 +512,8 @@ expand_kernel(const __grid_constant__ LoraArgs a) {
     // a block's steps lie apart, so that blocks side by side run over
     // neighbouring columns: step s covers the warp's 32 columns from here
     auto column = [&](int s) { return ((s * d.blocks + cb - d.first_block) * kWarps + warp) * 32; };
+    // each lane's own pieces of y, loaded two steps ahead: only their owner touches them
+    auto piece = [&](int s, int h, int q) { return smem + ((warp * kStages + s % kStages) * 4 + h * 2 + q) * 32 + lane; };
     auto prefetch = [&](int s) {
         const int nc = column(s) + t * 4;
         if (vec && s < a.steps) {
@@ -531,15 +521,26 @@ expand_kernel(const __grid_constant__ LoraArgs a) {
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    if (yrow[h] && nc + q * 16 < N) copy16(&ring[warp][s % kStages][h * 2 + q][lane], yrow[h] + nc + q * 16);
+                    if (yrow[h] && nc + q * 16 < N) copy16(piece(s, h, q), yrow[h] + nc + q * 16);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     prefetch(0);
     prefetch(1);
-    const int rank = a.ranks ? min(a.ranks[tile.adapter], R) : R, used = (rank + 7) / 8 * 8;
+    const int rank = tile.rank, used = (rank + 7) / 8 * 8;
     const W *B = static_cast<const W *>(d.B) + (int64_t)tile.adapter * R * N;
-    const float4 *v = a.v + (((int64_t)di * a.max_tiles + ti) * MB + mb) * (R16 / 16) * 64 + lane;
+    const int64_t part = (int64_t)a.max_tiles * MB * (R16 / 16) * 64;      // from one part of K to the next
+    const float4 *v = a.v + di * a.split * part + ((int64_t)ti * MB + mb) * (R16 / 16) * 64;
+    for (int i = tid; i < R16 * 4; i += kThreads) {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i / 64 * 16 + (i & 3) * 4 < used)                  // (behind that, shrink leaves nothing)
+            for (int s = 0; s < a.split; ++s) {
+                const float4 w = v[s * part + i];
+                f = make_float4(f.x + w.x, f.y + w.y, f.z + w.z, f.w + w.w);
+            }
+        vs[i] = f;
+    }
+    __syncthreads();
     for (int s = 0; s < a.steps; ++s) {
         const int n0 = column(s), nc = n0 + t * 4;
         if (n0 >= N) break;
@@ -549,11 +550,7 @@ expand_kernel(const __grid_constant__ LoraArgs a) {
         float acc[4][4] = {};                                  // [j][fragment]
         for (int r0 = 0; r0 < rank; r0 += 16) {
             const int r = r0 + t * 4;
-            float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
-            if (r < used) {
-                v0 = v[r0 * 4];
-                v1 = v[r0 * 4 + 32];
-            }
+            const float4 v0 = vs[r0 * 4 + lane], v1 = vs[r0 * 4 + 32 + lane];
             uint32_t w[4][4];                                  // [j][the lane's four ranks]
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -592,7 +589,7 @@ expand_kernel(const __grid_constant__ LoraArgs a) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
                     if (nc + q * 16 < N) {
-                        float4 f = ring[warp][s % kStages][h * 2 + q][lane];
+                        float4 f = *piece(s, h, q);
                         f.x += acc[q * 2][h * 2];
                         f.y += acc[q * 2][h * 2 + 1];
                         f.z += acc[q * 2 + 1][h * 2];
@@ -628,31 +625,64 @@ int steps_of(const bc_lora_desc *descs, int count, int64_t row_tiles) {
 }
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Scratch of one launch over `count` projections.
-size_t scratch(int count, int64_t M, int64_t R, int64_t adapters, int64_t S, bool f32) {
-    const int64_t T = tile_rows(M, S, f32), tiles = most_tiles(M, S, adapters, T), R16 = (R + 15) / 16 * 16;
-    return round256((size_t)kGroupRows * 4) + round256((size_t)tiles * sizeof(Tile)) +
-           (size_t)count * tiles * T * R16 * 4;
+// 32-rank chunks of a launch (neighbours that read the same x share a pass
+// over it), and the parts of K: about two blocks per SM, each with 1024 of K
+// or more.
+struct Shape {
+    int64_t T, tiles;
+    int chunks, split;
+};
+Shape shape_of(const bc_lora_desc *d, int count, int64_t M, int64_t R, int64_t adapters, int64_t S, bool f32) {
+    Shape s;
+    s.T = tile_rows(M, S, f32);
+    s.tiles = most_tiles(M, S, adapters, s.T);
+    s.chunks = 0;
+    int64_t K = 0;
+    for (int j = 0, n; j < count; j += n) {
+        for (n = 1; j + n < count && d[j + n].x == d[j].x && d[j + n].K == d[j].K;) ++n;
+        s.chunks += (int)((n * R + kChunk - 1) / kChunk);
+        K = d[j].K > K ? d[j].K : K;
+    }
+    s.split = 1;
+    while (s.split < kMaxSplit && s.tiles * s.chunks * s.split < 2 * kSms && K / s.split >= 1024) s.split *= 2;
+    return s;
+}
+// Scratch of one launch.
+size_t scratch(const Shape &s, int count, int64_t R) {
+    return round256((size_t)kGroupRows * 4) + round256((size_t)s.tiles * sizeof(Tile)) +
+           (size_t)count * s.split * s.tiles * s.T * ((R + 15) / 16 * 16) * 4;
+}
+
+// Lets the kernel have the shared memory of its largest rank (once per device).
+template <auto kKernel>
+bool allow_smem() {
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev])
+        done[dev] = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (kRing + kMaxRank * 4) * (int)sizeof(float4)) == cudaSuccess;
+    return done[dev];
 }
 
 template <typename X, typename W, int MB>
 bc_status launch(const LoraArgs &a, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.max_tiles * a.chunks * a.split));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = a.split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = a.split > 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, shrink_kernel<X, W, MB>, a);
+    if (!allow_smem<expand_kernel<W, MB>>()) return BC_ERR_CUDA;
+    shrink_kernel<X, W, MB><<<(unsigned)(a.max_tiles * a.chunks * a.split), kThreads, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) {
         // expand's blocks may start while shrink's finish; they wait for all of it before they read
+        cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(a.max_tiles * MB * a.col_blocks));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = (kRing + (a.R + 15) / 16 * 64) * sizeof(float4);
+        cfg.stream = s;
+        cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
         cfg.numAttrs = 1;
         e = cudaLaunchKernelEx(&cfg, expand_kernel<W, MB>, a);
     }
@@ -710,8 +740,13 @@ size_t bc_workspace_size_lora(const bc_lora_desc *descs, int count, int64_t M, i
                               int64_t n_adapters, int64_t n_segments, bc_dtype x_dtype) {
     bc_status st;
     if (!sizes_ok(descs, count, M, R, n_adapters, n_segments, &st)) return 0;
-    // launches of a call use the scratch in turn
-    return scratch(count < kMaxDescs ? count : kMaxDescs, M, R, n_adapters, n_segments, x_dtype == BC_F32);
+    size_t most = 0;
+    for (int i = 0; i < count; i += kMaxDescs) {           // launches of a call use the scratch in turn
+        const int n = count - i < kMaxDescs ? count - i : kMaxDescs;
+        const size_t b = scratch(shape_of(descs + i, n, M, R, n_adapters, n_segments, x_dtype == BC_F32), n, R);
+        most = b > most ? b : most;
+    }
+    return most;
 }
 
 bc_status bc_lora_add_batched(const bc_lora_desc *descs, int count, int64_t M, int64_t R,
@@ -756,36 +791,31 @@ bc_status bc_lora_add_batched(const bc_lora_desc *descs, int count, int64_t M, i
     a.S = (int)n_segments;
     a.R = (int)R;
     a.adapters = (int)n_adapters;
-    a.T = tile_rows(M, n_segments, x_dtype == BC_F32);
-    a.max_tiles = (int)most_tiles(M, n_segments, n_adapters, a.T);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.head = reinterpret_cast<int *>(ws);
     ws += round256((size_t)kGroupRows * 4);
     a.tiles = reinterpret_cast<Tile *>(ws);
-    a.v = reinterpret_cast<float4 *>(ws + round256((size_t)a.max_tiles * sizeof(Tile)));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     for (int i = 0; i < count; i += kMaxDescs) {
         a.count = count - i < kMaxDescs ? count - i : kMaxDescs;
-        a.col_blocks = a.chunks = 0;
-        a.steps = steps_of(descs + i, a.count, (int64_t)a.max_tiles * a.T / 16);
-        int64_t K = 0;
+        const Shape sh = shape_of(descs + i, a.count, M, R, n_adapters, n_segments, x_dtype == BC_F32);
+        a.T = (int)sh.T;
+        a.max_tiles = (int)sh.tiles;
+        a.chunks = sh.chunks;
+        a.split = sh.split;
+        a.v = reinterpret_cast<float4 *>(ws + round256((size_t)a.max_tiles * sizeof(Tile)));
+        a.col_blocks = 0;
+        a.steps = steps_of(descs + i, a.count, sh.tiles * sh.T / 16);
         for (int j = 0; j < a.count; ++j) {
             const bc_lora_desc &d = descs[i + j];
             const int blocks = (int)((d.N + kStep * a.steps - 1) / (kStep * a.steps));
             a.d[j] = Desc{d.x, d.A, d.B, d.y, (int)d.N, (int)d.K, 0, a.col_blocks, blocks};
             a.col_blocks += blocks;
-            K = d.K > K ? d.K : K;
         }
-        for (int j = 0, n; j < a.count; j += n) {          // neighbours that read the same x share a pass over it
+        for (int j = 0, n; j < a.count; j += n) {
             for (n = 1; j + n < a.count && a.d[j + n].x == a.d[j].x && a.d[j + n].K == a.d[j].K;) ++n;
             a.d[j].group_size = n;
-            a.chunks += (n * a.R + kChunk - 1) / kChunk;
         }
-        // parts of K: about two blocks per SM, each with 1024 of K or more (a
-        // part costs two cluster barriers, about 1.5 us)
-        a.split = 1;
-        while (a.split < kMaxSplit && (int64_t)a.max_tiles * a.chunks * a.split < 2 * kSms && K / a.split >= 1024)
-            a.split *= 2;
         if (x_dtype == BC_F32)
             st = w_dtype == BC_F16 ? launch<float, __half>(a, s) : launch<float, __nv_bfloat16>(a, s);
         else
