@@ -353,94 +353,97 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
                 if (lane == 0) reinterpret_cast<float *>(red)[(b * 32 + i * 4 + warp / 2) * 4 + (warp & 1)] = s;
             }
     } else {
+        // Rows and ranks that the tile lacks are taken from ones that it has:
+        // they only reach sums that no one reads.
+        const int nb = 32 - __clz(live);                       // (blocks below it may lack ranks)
         const W *arow[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            arow[b] = a_row(b, g);
-            if (arow[b]) arow[b] += t * 8;
+            const int vb = chunk * NB + min(b, nb - 1);
+            arow[b] = static_cast<const W *>(a.d[first + vb / R8].A) +
+                      ((int64_t)tile.adapter * R + vb % R8 * 8 + g) * K + t * 8;
         }
         const X *xrow[MB][2];
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                xrow[mb][h] = x_row(mb * 16 + g + h * 8);
-                if (xrow[mb][h]) xrow[mb][h] += t * 8;
-            }
-        auto load = [&](int u, uint4 (&wa)[NB], uint4 (&xa)[MB][2][kQ]) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-                wa[b] = arow[b] ? *reinterpret_cast<const uint4 *>(arow[b] + u * 32) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int q = 0; q < kQ; ++q)
-                        xa[mb][h][q] = xrow[mb][h] ? reinterpret_cast<const uint4 *>(xrow[mb][h] + u * 32)[q]
-                                                   : make_uint4(0, 0, 0, 0);
-        };
+            for (int h = 0; h < 2; ++h) xrow[mb][h] = x_row(min(mb * 16 + g + h * 8, n_rows - 1)) + t * 8;
         float acc[MB][NB][4] = {};
-        auto multiply = [&](const uint4 (&wa)[NB], const uint4 (&xa)[MB][2][kQ]) {
-            if constexpr (kBf16) {
+        auto run = [&](auto blocks_c) {
+            constexpr int L = decltype(blocks_c)::value;       // blocks of ranks
+            auto load = [&](int u, uint4 (&wa)[L], uint4 (&xa)[MB][2][kQ]) {
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb) {
-                    if (mb * 16 >= n_rows) break;
+                for (int b = 0; b < L; ++b) wa[b] = *reinterpret_cast<const uint4 *>(arow[b] + u * 32);
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const uint4 &p = xa[mb][0][0], &q = xa[mb][1][0];
-                        const uint32_t f[4] = {s ? p.z : p.x, s ? q.z : q.x, s ? p.w : p.y, s ? q.w : q.y};
+                for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-                        for (int b = 0; b < kChunk / 8; ++b)
-                            if (live >> b & 1) mma_bf16(acc[mb][b], f, s ? wa[b].z : wa[b].x, s ? wa[b].w : wa[b].y);
-                    }
-                }
-            } else {
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {              // two of the lane's eight k each
-                    uint32_t w0[kChunk / 8], w1[kChunk / 8];
+                        for (int q = 0; q < kQ; ++q)
+                            xa[mb][h][q] = reinterpret_cast<const uint4 *>(xrow[mb][h] + u * 32)[q];
+            };
+            auto multiply = [&](const uint4 (&wa)[L], const uint4 (&xa)[MB][2][kQ]) {
+                if constexpr (kBf16) {
 #pragma unroll
-                    for (int b = 0; b < kChunk / 8; ++b)
-                        widen<W>(s == 0 ? wa[b].x : s == 1 ? wa[b].y : s == 2 ? wa[b].z : wa[b].w, w0[b], w1[b]);
+                    for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-                    for (int mb = 0; mb < MB; ++mb) {
-                        if (mb * 16 >= n_rows) break;
-                        uint32_t hi[4], lo[4];
+                        for (int s = 0; s < 2; ++s) {
+                            const uint4 &p = xa[mb][0][0], &q = xa[mb][1][0];
+                            const uint32_t f[4] = {s ? p.z : p.x, s ? q.z : q.x, s ? p.w : p.y, s ? q.w : q.y};
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if constexpr (kF32) {
-                                const uint4 &p = xa[mb][h][s >> 1];
-                                split_tf32(__uint_as_float(s & 1 ? p.z : p.x), hi[h], lo[h]);
-                                split_tf32(__uint_as_float(s & 1 ? p.w : p.y), hi[h + 2], lo[h + 2]);
-                            } else {
-                                const uint4 &p = xa[mb][h][0];
-                                widen<__nv_bfloat16>(s == 0 ? p.x : s == 1 ? p.y : s == 2 ? p.z : p.w, hi[h], hi[h + 2]);
-                            }
+                            for (int b = 0; b < L; ++b)
+                                mma_bf16(acc[mb][b], f, s ? wa[b].z : wa[b].x, s ? wa[b].w : wa[b].y);
                         }
+                } else {
 #pragma unroll
-                        for (int b = 0; b < kChunk / 8; ++b)
-                            if (live >> b & 1) {
-                                if constexpr (kF32)
-                                    mma_tf32(acc[mb][b], lo[0], lo[1], lo[2], lo[3], w0[b], w1[b]);
+                    for (int s = 0; s < 4; ++s) {              // two of the lane's eight k each
+                        uint32_t w0[L], w1[L];
+#pragma unroll
+                        for (int b = 0; b < L; ++b)
+                            widen<W>(s == 0 ? wa[b].x : s == 1 ? wa[b].y : s == 2 ? wa[b].z : wa[b].w, w0[b], w1[b]);
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb) {
+                            uint32_t hi[4];
+                            [[maybe_unused]] uint32_t lo[4];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if constexpr (kF32) {
+                                    const uint4 &p = xa[mb][h][s >> 1];
+                                    split_tf32(__uint_as_float(s & 1 ? p.z : p.x), hi[h], lo[h]);
+                                    split_tf32(__uint_as_float(s & 1 ? p.w : p.y), hi[h + 2], lo[h + 2]);
+                                } else {
+                                    const uint4 &p = xa[mb][h][0];
+                                    widen<__nv_bfloat16>(s == 0 ? p.x : s == 1 ? p.y : s == 2 ? p.z : p.w, hi[h], hi[h + 2]);
+                                }
+                            }
+#pragma unroll
+                            for (int b = 0; b < L; ++b) {
+                                if constexpr (kF32) mma_tf32(acc[mb][b], lo[0], lo[1], lo[2], lo[3], w0[b], w1[b]);
                                 mma_tf32(acc[mb][b], hi[0], hi[1], hi[2], hi[3], w0[b], w1[b]);
                             }
+                        }
                     }
+                }
+            };
+            // the next step's pieces are on their way while this one's are multiplied
+            uint4 wa[2][L], xa[2][MB][2][kQ];
+            const int step = a.split * kWarps, units = K / 32;
+            int u = part * kWarps + warp;
+            if (u < units) load(u, wa[0], xa[0]);
+            for (; u < units; u += 2 * step) {
+                if (u + step < units) load(u + step, wa[1], xa[1]);
+                multiply(wa[0], xa[0]);
+                if (u + step < units) {
+                    if (u + 2 * step < units) load(u + 2 * step, wa[0], xa[0]);
+                    multiply(wa[1], xa[1]);
                 }
             }
         };
-        // the next step's pieces are on their way while this one's are multiplied
-        uint4 wa[2][NB], xa[2][MB][2][kQ];
-        const int step = a.split * kWarps, units = K / 32;
-        int u = part * kWarps + warp;
-        if (u < units) load(u, wa[0], xa[0]);
-        for (; u < units; u += 2 * step) {
-            if (u + step < units) load(u + step, wa[1], xa[1]);
-            multiply(wa[0], xa[0]);
-            if (u + step < units) {
-                if (u + 2 * step < units) load(u + 2 * step, wa[0], xa[0]);
-                multiply(wa[1], xa[1]);
-            }
-        }
+        static_assert(NB == 4, "one case per number of blocks");
+        if (nb == 4) run(std::integral_constant<int, 4>());
+        else if (nb == 3) run(std::integral_constant<int, 3>());
+        else if (nb == 2) run(std::integral_constant<int, 2>());
+        else run(std::integral_constant<int, 1>());
         // the block's sum over its warps, in fragment order
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
@@ -468,10 +471,13 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
     for (int i = tid; i < kQuads; i += kThreads) {
         const int mb = i / 32 / NB, vb = chunk * NB + i / 32 % NB, rb = vb % R8;
         if (vb >= blocks || rb >= used || mb * 16 >= n_rows) continue;
-        const float4 s = red[i];
+        float4 s = red[i];
         const int l = i & 31, q = rb / 2, lq = (rb & 1) * 2 + (l & 3) / 2;
         const int64_t at = ((int64_t)(first + vb / R8) * a.split + part) * a.max_tiles + ti;
         float2 *out = reinterpret_cast<float2 *>(a.v + ((at * MB + mb) * (R16 / 16) + q) * 64 + (l >> 2) * 4 + lq) + (l & 1);
+        // ranks behind the adapter's count as 0 (whatever A holds there)
+        if (rb * 8 + (l & 3) * 2 >= rank) s.x = s.z = 0.f;
+        if (rb * 8 + (l & 3) * 2 + 1 >= rank) s.y = s.w = 0.f;
         out[0] = make_float2(s.x * tile.scale, s.y * tile.scale);
         out[64] = make_float2(s.z * tile.scale, s.w * tile.scale);
     }
@@ -531,6 +537,18 @@ expand_kernel(const __grid_constant__ LoraArgs a) {
     const W *B = static_cast<const W *>(d.B) + (int64_t)tile.adapter * R * N;
     const int64_t part = (int64_t)a.max_tiles * MB * (R16 / 16) * 64;      // from one part of K to the next
     const float4 *v = a.v + di * a.split * part + ((int64_t)ti * MB + mb) * (R16 / 16) * 64;
+    // B's next pieces are on their way while the last ones are multiplied
+    uint2 ahead[4];
+    auto fetch = [&](int s, int r0) {
+        const int n0 = column(s), r = r0 + t * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = n0 + (j >> 1) * 16 + (g >> 1) * 4 + (j & 1) * 2 + (g & 1);
+            ahead[j] = s < a.steps && n < N && r < rank ? *reinterpret_cast<const uint2 *>(B + (int64_t)n * R + r)
+                                                        : make_uint2(0, 0);
+        }
+    };
+    fetch(0, 0);
     for (int i = tid; i < R16 * 4; i += kThreads) {
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i / 64 * 16 + (i & 3) * 4 < used)                  // (behind that, shrink leaves nothing)
@@ -554,15 +572,14 @@ expand_kernel(const __grid_constant__ LoraArgs a) {
             uint32_t w[4][4];                                  // [j][the lane's four ranks]
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int n = n0 + (j >> 1) * 16 + (g >> 1) * 4 + (j & 1) * 2 + (g & 1);
-                uint2 q = make_uint2(0, 0);
-                if (n < N && r < rank) q = *reinterpret_cast<const uint2 *>(B + (int64_t)n * R + r);
-                widen<W>(q.x, w[j][0], w[j][1]);
-                widen<W>(q.y, w[j][2], w[j][3]);
+                widen<W>(ahead[j].x, w[j][0], w[j][1]);
+                widen<W>(ahead[j].y, w[j][2], w[j][3]);
 #pragma unroll
                 for (int e = 1; e < 4; ++e)
                     if (r + e >= rank) w[j][e] = 0;            // behind the adapter's rank: not its values
             }
+            if (r0 + 16 < rank) fetch(s, r0 + 16);
+            else fetch(s + 1, 0);
             uint32_t h0[4], h1[4], l0[4], l1[4];
             split_tf32(v0.x, h0[0], l0[0]);
             split_tf32(v0.y, h0[1], l0[1]);
