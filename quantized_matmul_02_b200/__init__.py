@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -398,6 +399,10 @@ def _elsewhere(what: str, dev: int, stream: Optional[torch.cuda.Stream]):
     return None if dev == _current_device() else torch.cuda.device(dev)
 
 
+def _scratch(nbytes: int, device) -> torch.Tensor:
+    return torch.empty_strided((nbytes,), (1,), dtype=_U8, device=device)
+
+
 def _p(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -519,7 +524,7 @@ def make_lora_descs(items: Sequence[tuple]) -> LoraDescs:
     d = LoraDescs()
     d.M, d.n_adapters, d.R, d.count, d.device = M, n, R, len(items), dev
     d.x_dtype, d.w_dtype, d.tensors = _DT[xt], _DT[wt], items
-    d.array = (ctypes.c_int64 * len(fields))(*fields)       # bc_lora_desc: six 8-byte fields
+    d.array = struct.pack(f"{len(fields)}q", *fields)       # bc_lora_desc: six 8-byte fields
     return d
 
 
@@ -554,7 +559,7 @@ def lora_add_batched(descs: LoraDescs, seg_start: torch.Tensor, seg_adapter: tor
         with other:
             return lora_add_batched(descs, seg_start, seg_adapter, ranks, scaling, workspace)
     if workspace is None:
-        workspace = torch.empty(workspace_size_lora(descs, S), dtype=_U8, device=seg_start.device)
+        workspace = _scratch(workspace_size_lora(descs, S), seg_start.device)
     _check(lib.bc_lora_add_batched(descs.array, descs.count, descs.M, descs.R, n, descs.x_dtype,
                                    descs.w_dtype, seg_start.data_ptr(), seg_adapter.data_ptr(), S,
                                    _p(ranks), _p(scaling), workspace.data_ptr(), workspace.nbytes,
@@ -578,8 +583,11 @@ def workspace_size_beam(batch: int, beams: int, V: int, n_out: int) -> int:
 def _beam_out(what, device, batch, n_out, out):
     shape = (batch, n_out)
     if out is None:
-        return (torch.empty(shape, dtype=_F32, device=device), torch.empty(shape, dtype=_I32, device=device),
-                torch.empty(shape, dtype=_I32, device=device), torch.empty(shape, dtype=_U8, device=device))
+        if batch <= 0 or n_out <= 0:
+            raise ValueError(f"{what}: nothing to select")
+        parent = torch.empty_strided(shape, (n_out, 1), dtype=_I32, device=device)
+        return (torch.empty_like(parent, dtype=_F32), parent, torch.empty_like(parent),
+                torch.empty_like(parent, dtype=_U8))
     for t, name, dt in zip(out, ("out scores", "parent", "token", "out finished"),
                            (_F32, _I32, _I32, _U8)):
         _want(what, name, t, shape, dt)
@@ -610,8 +618,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int,
             return beam_select(logits, scores, n_out, finished, eos, pad, out, workspace)
     o = _beam_out(what, logits.device, batch, n_out, out)
     if workspace is None:
-        workspace = torch.empty(lib.bc_workspace_size_beam(batch, beams, V, n_out), dtype=_U8,
-                                device=logits.device)
+        workspace = _scratch(lib.bc_workspace_size_beam(batch, beams, V, n_out), logits.device)
     _check(lib.bc_beam_select(logits.data_ptr(), scores.data_ptr(), _p(finished), batch, beams, V,
                               n_out, eos, pad, o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr(),
                               o[3].data_ptr(), workspace.data_ptr(), workspace.nbytes,
@@ -661,7 +668,7 @@ def matmul_q_beam(x: torch.Tensor, W: torch.Tensor, scales: Optional[torch.Tenso
     o = _beam_out(what, x.device, batch, n_out, out)
     if workspace is None:
         need = workspace_size_matmul_beam(batch, beams, N, K, n_out, mode, _DT[x.dtype])
-        workspace = torch.empty(need, dtype=_U8, device=x.device)
+        workspace = _scratch(need, x.device)
     _check(lib.bc_matmul_q_beam(x.data_ptr(), _DT[x.dtype], W.data_ptr(), _p(scales), _p(zeros),
                                 batch, beams, N, K, bits, group, mode, beam_scores.data_ptr(),
                                 _p(finished), n_out, eos, pad, o[0].data_ptr(), o[1].data_ptr(),
@@ -712,7 +719,7 @@ def make_beam_states(tensors: Sequence[torch.Tensor]) -> BeamStates:
         fields += (t.data_ptr(), rows, run * size, row_stride * size, beam * size)
     st = BeamStates()
     st.beams_total, st.device, st.tensors, st.count = total, dev, tensors, len(tensors)
-    st.array = (ctypes.c_int64 * len(fields))(*fields)      # bc_beam_state: five 8-byte fields
+    st.array = struct.pack(f"{len(fields)}q", *fields)      # bc_beam_state: five 8-byte fields
     return st
 
 

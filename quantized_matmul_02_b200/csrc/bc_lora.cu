@@ -41,6 +41,7 @@ constexpr int kFew = 2;                // rows up to here: plain products instea
 constexpr int kMaxSplit = 8;           // parts of K
 constexpr int kStep = kWarps * 32;     // columns an expand block takes at a time
 constexpr int kMaxSteps = 12;          // such steps per block
+constexpr int kAhead = 2;              // 16-rank pieces of B on their way, for more than 16 ranks
 constexpr int kStages = 3;             // of which y is on its way
 constexpr int kRing = kWarps * kStages * 4 * 32;   // 16-byte pieces of y in shared memory
 
@@ -483,27 +484,24 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
     }
 }
 
-__device__ __forceinline__ void copy16(float4 *to, const float *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
-                 : "memory");
+template <int BYTES, typename T>
+__device__ __forceinline__ void copy(T *to, const float *from) {
+    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s), "l"(from) : "memory");
 }
 
-// grid: tiles x MB x column blocks of all projections
-template <typename W, int MB>
-__global__ void __launch_bounds__(kThreads, 3)
-expand_kernel(const __grid_constant__ LoraArgs a) {
+// VEC: y in 16-byte pieces.  AHEAD: pieces of 16 ranks of B that are loaded
+// before the last ones are multiplied.
+template <typename W, bool VEC, int AHEAD>
+__device__ __forceinline__ void expand(const LoraArgs &a, const Desc &d, int di, int ti, int mb, int mbs,
+                                       int cb, const Tile &tile) {
     extern __shared__ __align__(16) float4 smem[];
     float4 *const vs = smem + kRing;                           // v of the 16 rows: [R16 / 16][2][32]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int sub = blockIdx.x / a.col_blocks, cb = blockIdx.x - sub * a.col_blocks;
-    const int ti = sub / MB, mb = sub - ti * MB;
-    int di = 0;
-    while (di + 1 < a.count && cb >= a.d[di + 1].first_block) ++di;
-    const Desc &d = a.d[di];
     const int N = d.N, R = a.R, R16 = (R + 15) / 16 * 16;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Tile tile = a.tiles[ti];
-    if (mb * 16 >= tile.rows || tile.rank == 0) return;
     float *yrow[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -514,20 +512,38 @@ expand_kernel(const __grid_constant__ LoraArgs a) {
             yrow[h] = d.y + m * N;
         }
     }
-    const bool vec = (N & 3) == 0 && (reinterpret_cast<uintptr_t>(d.y) & 15) == 0;
     // a block's steps lie apart, so that blocks side by side run over
     // neighbouring columns: step s covers the warp's 32 columns from here
-    auto column = [&](int s) { return ((s * d.blocks + cb - d.first_block) * kWarps + warp) * 32; };
-    // each lane's own pieces of y, loaded two steps ahead: only their owner touches them
+    auto column = [&](int s) { return ((s * d.blocks + cb) * kWarps + warp) * 32; };
+    // Column 2 t + i of fragment block j, among the 32: with 16-byte accesses a
+    // lane holds 4 neighbours twice, with 4-byte ones four lanes hold neighbours;
+    // either way an access takes whole sectors or their halves.
+    auto col = [&](int j, int t, int i) {
+        return VEC ? (j >> 1) * 16 + t * 4 + (j & 1) * 2 + i : (j * 2 + i) * 4 + t;
+    };
+    // Each lane's own pieces of y are loaded two steps ahead; only their owner
+    // touches them.
     auto piece = [&](int s, int h, int q) { return smem + ((warp * kStages + s % kStages) * 4 + h * 2 + q) * 32 + lane; };
+    auto single = [&](int s, int h, int e) {
+        return reinterpret_cast<float *>(smem + (warp * kStages + s % kStages) * 4 * 32) + (h * 8 + e) * 32 + lane;
+    };
     auto prefetch = [&](int s) {
-        const int nc = column(s) + t * 4;
-        if (vec && s < a.steps) {
+        const int n0 = column(s);
+        if (s < a.steps) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                if (!yrow[h]) continue;
+                if constexpr (VEC) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (yrow[h] && nc + q * 16 < N) copy16(piece(s, h, q), yrow[h] + nc + q * 16);
+                    for (int q = 0; q < 2; ++q)
+                        if (n0 + col(q * 2, t, 0) < N) copy<16>(piece(s, h, q), yrow[h] + n0 + col(q * 2, t, 0));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (n0 + col(e >> 1, t, e & 1) < N)
+                            copy<4>(single(s, h, e), yrow[h] + n0 + col(e >> 1, t, e & 1));
+                }
+            }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -535,17 +551,19 @@ expand_kernel(const __grid_constant__ LoraArgs a) {
     prefetch(1);
     const int rank = tile.rank, used = (rank + 7) / 8 * 8;
     const W *B = static_cast<const W *>(d.B) + (int64_t)tile.adapter * R * N;
-    const int64_t part = (int64_t)a.max_tiles * MB * (R16 / 16) * 64;      // from one part of K to the next
-    const float4 *v = a.v + di * a.split * part + ((int64_t)ti * MB + mb) * (R16 / 16) * 64;
-    // B's next pieces are on their way while the last ones are multiplied
-    uint2 ahead[4];
+    const int64_t part = (int64_t)a.max_tiles * mbs * (R16 / 16) * 64;      // from one part of K to the next
+    const float4 *v = a.v + di * a.split * part + ((int64_t)ti * mbs + mb) * (R16 / 16) * 64;
+    uint2 ahead[AHEAD][4];
     auto fetch = [&](int s, int r0) {
         const int n0 = column(s), r = r0 + t * 4;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int n = n0 + (j >> 1) * 16 + (g >> 1) * 4 + (j & 1) * 2 + (g & 1);
-            ahead[j] = s < a.steps && n < N && r < rank ? *reinterpret_cast<const uint2 *>(B + (int64_t)n * R + r)
-                                                        : make_uint2(0, 0);
+            const int n = n0 + col(j, g >> 1, g & 1);
+            const W *p = B + (int64_t)n * R + r;
+            const bool in = s < a.steps && n < N;
+#pragma unroll
+            for (int c = 0; c < AHEAD; ++c)
+                ahead[c][j] = in && r + c * 16 < rank ? *reinterpret_cast<const uint2 *>(p + c * 16) : make_uint2(0, 0);
         }
     };
     fetch(0, 0);
@@ -560,68 +578,103 @@ expand_kernel(const __grid_constant__ LoraArgs a) {
     }
     __syncthreads();
     for (int s = 0; s < a.steps; ++s) {
-        const int n0 = column(s), nc = n0 + t * 4;
+        const int n0 = column(s);
         if (n0 >= N) break;
         prefetch(s + 2);
-        // y += B v: column 2 t + i of block j is column j / 2 * 16 + t * 4 + j % 2 * 2 + i of
-        // the 32, so that a lane holds 4 neighbours twice and 4 lanes whole sectors
         float acc[4][4] = {};                                  // [j][fragment]
-        for (int r0 = 0; r0 < rank; r0 += 16) {
-            const int r = r0 + t * 4;
-            const float4 v0 = vs[r0 * 4 + lane], v1 = vs[r0 * 4 + 32 + lane];
-            uint32_t w[4][4];                                  // [j][the lane's four ranks]
+        for (int r0 = 0; r0 < rank; r0 += 16 * AHEAD) {
+            uint2 now[AHEAD][4];
+            auto fetch_next = [&] {
+                if (r0 + 16 * AHEAD < rank) fetch(s, r0 + 16 * AHEAD);
+                else fetch(s + 1, 0);
+            };
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                widen<W>(ahead[j].x, w[j][0], w[j][1]);
-                widen<W>(ahead[j].y, w[j][2], w[j][3]);
+            for (int c = 0; c < AHEAD; ++c)
 #pragma unroll
-                for (int e = 1; e < 4; ++e)
-                    if (r + e >= rank) w[j][e] = 0;            // behind the adapter's rank: not its values
-            }
-            if (r0 + 16 < rank) fetch(s, r0 + 16);
-            else fetch(s + 1, 0);
-            uint32_t h0[4], h1[4], l0[4], l1[4];
-            split_tf32(v0.x, h0[0], l0[0]);
-            split_tf32(v0.y, h0[1], l0[1]);
-            split_tf32(v0.z, h0[2], l0[2]);
-            split_tf32(v0.w, h0[3], l0[3]);
-            split_tf32(v1.x, h1[0], l1[0]);
-            split_tf32(v1.y, h1[1], l1[1]);
-            split_tf32(v1.z, h1[2], l1[2]);
-            split_tf32(v1.w, h1[3], l1[3]);
+                for (int j = 0; j < 4; ++j) now[c][j] = ahead[c][j];
+            if constexpr (AHEAD > 1) fetch_next();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                mma_tf32(acc[j], l0[0], l1[0], l0[1], l1[1], w[j][0], w[j][1]);
-                mma_tf32(acc[j], l0[2], l1[2], l0[3], l1[3], w[j][2], w[j][3]);
-                mma_tf32(acc[j], h0[0], h1[0], h0[1], h1[1], w[j][0], w[j][1]);
-                mma_tf32(acc[j], h0[2], h1[2], h0[3], h1[3], w[j][2], w[j][3]);
+            for (int c = 0; c < AHEAD; ++c) {
+                const int rc = r0 + c * 16, r = rc + t * 4;
+                if (rc >= rank) break;
+                const float4 v0 = vs[rc * 4 + lane], v1 = vs[rc * 4 + 32 + lane];
+                uint32_t w[4][4];                              // [j][the lane's four ranks]
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    widen<W>(now[c][j].x, w[j][0], w[j][1]);
+                    widen<W>(now[c][j].y, w[j][2], w[j][3]);
+                }
+                if (rc + 16 > rank)                            // behind the adapter's rank: not its values
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 1; e < 4; ++e)
+                            if (r + e >= rank) w[j][e] = 0;
+                if constexpr (AHEAD == 1) fetch_next();        // (in the registers that `now` leaves)
+                uint32_t h0[4], h1[4], l0[4], l1[4];
+                split_tf32(v0.x, h0[0], l0[0]);
+                split_tf32(v0.y, h0[1], l0[1]);
+                split_tf32(v0.z, h0[2], l0[2]);
+                split_tf32(v0.w, h0[3], l0[3]);
+                split_tf32(v1.x, h1[0], l1[0]);
+                split_tf32(v1.y, h1[1], l1[1]);
+                split_tf32(v1.z, h1[2], l1[2]);
+                split_tf32(v1.w, h1[3], l1[3]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    mma_tf32(acc[j], l0[0], l1[0], l0[1], l1[1], w[j][0], w[j][1]);
+                    mma_tf32(acc[j], l0[2], l1[2], l0[3], l1[3], w[j][2], w[j][3]);
+                    mma_tf32(acc[j], h0[0], h1[0], h0[1], h1[1], w[j][0], w[j][1]);
+                    mma_tf32(acc[j], h0[2], h1[2], h0[3], h1[3], w[j][2], w[j][3]);
+                }
             }
         }
         asm volatile("cp.async.wait_group 2;" ::: "memory");
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (!yrow[h]) continue;
-            float *p = yrow[h] + nc;
-            if (vec) {
+            float *p = yrow[h] + n0;
+            if constexpr (VEC) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (nc + q * 16 < N) {
+                for (int q = 0; q < 2; ++q) {
+                    const int c = col(q * 2, t, 0);
+                    if (n0 + c < N) {
                         float4 f = *piece(s, h, q);
                         f.x += acc[q * 2][h * 2];
                         f.y += acc[q * 2][h * 2 + 1];
                         f.z += acc[q * 2 + 1][h * 2];
                         f.w += acc[q * 2 + 1][h * 2 + 1];
-                        *reinterpret_cast<float4 *>(p + q * 16) = f;
+                        *reinterpret_cast<float4 *>(p + c) = f;
                     }
+                }
             } else {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int c = (q >> 2) * 16 + (q & 3);
-                    if (nc + c < N) p[c] += acc[q >> 1][h * 2 + (q & 1)];
+                for (int e = 0; e < 8; ++e) {
+                    const int c = col(e >> 1, t, e & 1);
+                    if (n0 + c < N) p[c] = *single(s, h, e) + acc[e >> 1][h * 2 + (e & 1)];
                 }
             }
         }
     }
+}
+
+// grid: tiles x blocks of 16 rows x column blocks of all projections
+template <typename W, int AHEAD>
+__global__ void __launch_bounds__(kThreads, AHEAD == 1 ? 3 : 2)
+expand_kernel(const __grid_constant__ LoraArgs a) {
+    const int mbs = a.T / 16;
+    const int sub = blockIdx.x / a.col_blocks, cb = blockIdx.x - sub * a.col_blocks;
+    const int ti = sub / mbs, mb = sub - ti * mbs;
+    int di = 0;
+    while (di + 1 < a.count && cb >= a.d[di + 1].first_block) ++di;
+    const Desc &d = a.d[di];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Tile tile = a.tiles[ti];
+    if (mb * 16 >= tile.rows || tile.rank == 0) return;
+    if ((d.N & 3) == 0 && (reinterpret_cast<uintptr_t>(d.y) & 15) == 0)
+        expand<W, true, AHEAD>(a, d, di, ti, mb, mbs, cb - d.first_block, tile);
+    else
+        expand<W, false, AHEAD>(a, d, di, ti, mb, mbs, cb - d.first_block, tile);
 }
 
 // Tile height: 16 rows while rows are few or segments short, else 32; fp32
@@ -686,7 +739,9 @@ bool allow_smem() {
 
 template <typename X, typename W, int MB>
 bc_status launch(const LoraArgs &a, cudaStream_t s) {
-    if (!allow_smem<expand_kernel<W, MB>>()) return BC_ERR_CUDA;
+    // 64 ranks of B ahead where there are that many: a block's steps wait for B otherwise
+    const auto expand = a.R <= 16 ? expand_kernel<W, 1> : expand_kernel<W, kAhead>;
+    if (!(a.R <= 16 ? allow_smem<expand_kernel<W, 1>>() : allow_smem<expand_kernel<W, kAhead>>())) return BC_ERR_CUDA;
     shrink_kernel<X, W, MB><<<(unsigned)(a.max_tiles * a.chunks * a.split), kThreads, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) {
@@ -701,7 +756,7 @@ bc_status launch(const LoraArgs &a, cudaStream_t s) {
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, expand_kernel<W, MB>, a);
+        e = cudaLaunchKernelEx(&cfg, expand, a);
     }
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
