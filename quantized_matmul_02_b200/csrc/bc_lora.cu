@@ -18,9 +18,10 @@
 // are small beside them up to R = 128.
 //
 // Precision: fp32 throughout.  Products of 16-bit values are exact in the
-// tensor cores (bf16 with bf16, or tf32, which holds bf16 and fp16 exactly);
-// an fp32 x, and v, go in as two tf32 pieces, 2^-22 of the value away.
-// Sums run in a fixed order: results do not change from call to call.
+// tensor cores (of one type, or in tf32, which holds bf16 and fp16 exactly).
+// An fp32 x goes in as two tf32 pieces, 2^-22 of the value away; v as two or
+// three pieces of B's own type, as near, so that B needs no conversion.  Sums
+// run in a fixed order: results do not change from call to call.
 #include "bc_internal.cuh"
 
 #include <mutex>
@@ -40,7 +41,7 @@ constexpr int kChunk = 32;             // ranks per shrink block
 constexpr int kFew = 2;                // rows up to here: plain products instead of fragments
 constexpr int kMaxSplit = 8;           // parts of K
 constexpr int kStep = kWarps * 32;     // columns an expand block takes at a time
-constexpr int kMaxSteps = 12;          // such steps per block
+constexpr int kMaxSteps = 6;          // such steps per block
 constexpr int kAhead = 2;              // 16-rank pieces of B on their way, for more than 16 ranks
 constexpr int kStages = 3;             // of which y is on its way
 constexpr int kRing = kWarps * kStages * 4 * 32;   // 16-byte pieces of y in shared memory
@@ -80,6 +81,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+                 "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
@@ -92,6 +99,27 @@ __device__ __forceinline__ void split_tf32(float f, uint32_t &hi, uint32_t &lo) 
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(f));
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(f - __uint_as_float(hi)));
 }
+// Two values' leading piece in W's type, packed; the values lose it.
+template <typename W>
+__device__ __forceinline__ uint32_t take_piece(float &a, float &b) {
+    if constexpr (std::is_same<W, __half>::value) {
+        const __half2 h = __floats2half2_rn(a, b);
+        const float2 f = __half22float2(h);
+        a -= f.x;
+        b -= f.y;
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        const uint32_t u = *reinterpret_cast<const uint32_t *>(&h);
+        a -= __uint_as_float(u << 16);
+        b -= __uint_as_float(u & 0xffff0000u);
+        return u;
+    }
+}
+// Pieces of an fp32 v in B's type: three of bf16 (2^-25 of the value away), two
+// of fp16 (2^-22, after the row is scaled by a power of two).
+template <typename W>
+constexpr int kPieces = std::is_same<W, __half>::value ? 2 : 3;
 // Two 16-bit values as fp32 bits.
 template <typename W>
 __device__ __forceinline__ void widen(uint32_t u, uint32_t &a, uint32_t &b) {
@@ -499,7 +527,10 @@ template <typename W, bool VEC, int AHEAD>
 __device__ __forceinline__ void expand(const LoraArgs &a, const Desc &d, int di, int ti, int mb, int mbs,
                                        int cb, const Tile &tile) {
     extern __shared__ __align__(16) float4 smem[];
-    float4 *const vs = smem + kRing;                           // v of the 16 rows: [R16 / 16][2][32]
+    constexpr int P = kPieces<W>;
+    constexpr bool kHalf = std::is_same<W, __half>::value;
+    uint4 *const vs = reinterpret_cast<uint4 *>(smem + kRing);  // v of the 16 rows: [R16 / 16][P][32] fragments
+    __shared__ uint32_t top[16];                               // fp16: largest |v| of each row, as bits
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int N = d.N, R = a.R, R16 = (R + 15) / 16 * 16;
     float *yrow[2];
@@ -567,16 +598,54 @@ __device__ __forceinline__ void expand(const LoraArgs &a, const Desc &d, int di,
         }
     };
     fetch(0, 0);
-    for (int i = tid; i < R16 * 4; i += kThreads) {
+    constexpr int kMine = kMaxRank * 4 / kThreads;             // quads of ranks that a thread joins
+    float4 mine[kMine];
+    if (kHalf) {
+        if (tid < 16) top[tid] = 0;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int c = 0; c < kMine; ++c) {
+        const int i = c * kThreads + tid;                      // place (q, h, lane): row lane / 4 + 8 h, ranks q * 16 + ...
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i / 64 * 16 + (i & 3) * 4 < used)                  // (behind that, shrink leaves nothing)
+        if (i < R16 * 4 && i / 64 * 16 + (i & 3) * 4 < used)   // (behind that, shrink leaves nothing)
             for (int s = 0; s < a.split; ++s) {
                 const float4 w = v[s * part + i];
                 f = make_float4(f.x + w.x, f.y + w.y, f.z + w.z, f.w + w.w);
             }
-        vs[i] = f;
+        mine[c] = f;
+        if (kHalf && i < R16 * 4)
+            atomicMax(&top[(i >> 2 & 7) + (i >> 5 & 1) * 8],
+                      __float_as_uint(fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w)))));
+    }
+    // fp16 pieces are taken of v times 2^(141 - e), e the exponent bits of the
+    // row's largest: that one lies in 2^14 .. 2^15, and a piece's least step
+    // is 2^-40 of it.
+    auto exponent = [&](int row) { return max((int)(top[row] >> 23), 15); };
+    if (kHalf) __syncthreads();
+#pragma unroll
+    for (int c = 0; c < kMine; ++c) {
+        const int i = c * kThreads + tid;
+        if (i >= R16 * 4) break;
+        float4 f = mine[c];
+        const int h = i >> 5 & 1, l = i & 31;
+        if (kHalf) {
+            const float scale = __uint_as_float((uint32_t)(141 + 127 - exponent((l >> 2) + h * 8)) << 23);
+            f = make_float4(f.x * scale, f.y * scale, f.z * scale, f.w * scale);
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            uint32_t *to = reinterpret_cast<uint32_t *>(vs + (i / 64 * P + p) * 32 + l) + h;
+            to[0] = take_piece<W>(f.x, f.y);
+            to[2] = take_piece<W>(f.z, f.w);
+        }
     }
     __syncthreads();
+    float unscale[2] = {1.f, 1.f};
+    if (kHalf) {
+        unscale[0] = __uint_as_float((uint32_t)(exponent(g) - 141 + 127) << 23);
+        unscale[1] = __uint_as_float((uint32_t)(exponent(g + 8) - 141 + 127) << 23);
+    }
     for (int s = 0; s < a.steps; ++s) {
         const int n0 = column(s);
         if (n0 >= N) break;
@@ -584,51 +653,39 @@ __device__ __forceinline__ void expand(const LoraArgs &a, const Desc &d, int di,
         float acc[4][4] = {};                                  // [j][fragment]
         for (int r0 = 0; r0 < rank; r0 += 16 * AHEAD) {
             uint2 now[AHEAD][4];
-            auto fetch_next = [&] {
-                if (r0 + 16 * AHEAD < rank) fetch(s, r0 + 16 * AHEAD);
-                else fetch(s + 1, 0);
-            };
 #pragma unroll
             for (int c = 0; c < AHEAD; ++c)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) now[c][j] = ahead[c][j];
-            if constexpr (AHEAD > 1) fetch_next();
+            if (r0 + 16 * AHEAD < rank) fetch(s, r0 + 16 * AHEAD);
+            else fetch(s + 1, 0);
 #pragma unroll
             for (int c = 0; c < AHEAD; ++c) {
                 const int rc = r0 + c * 16, r = rc + t * 4;
                 if (rc >= rank) break;
-                const float4 v0 = vs[rc * 4 + lane], v1 = vs[rc * 4 + 32 + lane];
-                uint32_t w[4][4];                              // [j][the lane's four ranks]
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    widen<W>(now[c][j].x, w[j][0], w[j][1]);
-                    widen<W>(now[c][j].y, w[j][2], w[j][3]);
-                }
                 if (rc + 16 > rank)                            // behind the adapter's rank: not its values
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 4; ++j) {
+                        now[c][j].x &= r + 1 < rank ? 0xffffffffu : r < rank ? 0xffffu : 0u;
+                        now[c][j].y &= r + 3 < rank ? 0xffffffffu : r + 2 < rank ? 0xffffu : 0u;
+                    }
 #pragma unroll
-                        for (int e = 1; e < 4; ++e)
-                            if (r + e >= rank) w[j][e] = 0;
-                if constexpr (AHEAD == 1) fetch_next();        // (in the registers that `now` leaves)
-                uint32_t h0[4], h1[4], l0[4], l1[4];
-                split_tf32(v0.x, h0[0], l0[0]);
-                split_tf32(v0.y, h0[1], l0[1]);
-                split_tf32(v0.z, h0[2], l0[2]);
-                split_tf32(v0.w, h0[3], l0[3]);
-                split_tf32(v1.x, h1[0], l1[0]);
-                split_tf32(v1.y, h1[1], l1[1]);
-                split_tf32(v1.z, h1[2], l1[2]);
-                split_tf32(v1.w, h1[3], l1[3]);
+                for (int p = P - 1; p >= 0; --p) {
+                    const uint4 q = vs[(rc / 16 * P + p) * 32 + lane];
+                    const uint32_t f[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    mma_tf32(acc[j], l0[0], l1[0], l0[1], l1[1], w[j][0], w[j][1]);
-                    mma_tf32(acc[j], l0[2], l1[2], l0[3], l1[3], w[j][2], w[j][3]);
-                    mma_tf32(acc[j], h0[0], h1[0], h0[1], h1[1], w[j][0], w[j][1]);
-                    mma_tf32(acc[j], h0[2], h1[2], h0[3], h1[3], w[j][2], w[j][3]);
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (kHalf) mma_f16(acc[j], f, now[c][j].x, now[c][j].y);
+                        else mma_bf16(acc[j], f, now[c][j].x, now[c][j].y);
+                    }
                 }
             }
         }
+        if (kHalf)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][e] *= unscale[e >> 1];
         asm volatile("cp.async.wait_group 2;" ::: "memory");
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -733,7 +790,7 @@ bool allow_smem() {
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev])
         done[dev] = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (kRing + kMaxRank * 4) * (int)sizeof(float4)) == cudaSuccess;
+                                         (kRing + kMaxRank / 16 * 3 * 32) * (int)sizeof(float4)) == cudaSuccess;
     return done[dev];
 }
 
@@ -749,7 +806,7 @@ bc_status launch(const LoraArgs &a, cudaStream_t s) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(a.max_tiles * MB * a.col_blocks));
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = (kRing + (a.R + 15) / 16 * 64) * sizeof(float4);
+        cfg.dynamicSmemBytes = (kRing + (a.R + 15) / 16 * kPieces<W> * 32) * sizeof(float4);
         cfg.stream = s;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
