@@ -169,6 +169,7 @@ norm_kernel(const NormArgs a) {
         return VEC ? (c * TPR + t) * 8 + i : c * TPR * 8 + i * TPR + t;
     };
     float ss = 0.f;
+    Raw8 rw[CH];                                 // the weights are on their way during the sum
     if constexpr (VEC) {
         Raw8 rx[CH], rr[CH];
 #pragma unroll
@@ -176,6 +177,7 @@ norm_kernel(const NormArgs a) {
             if (live && col(c, 0) < a.D) {
                 rx[c] = load8(a.x, base + col(c, 0), a.xt);
                 if (a.res) rr[c] = load8(a.res, base + col(c, 0), a.rt);
+                if (a.w) rw[c] = load8(a.w, col(c, 0), a.wt);
             }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -228,7 +230,7 @@ norm_kernel(const NormArgs a) {
             const bool in = live && col(c, 0) < a.D;
             float wv[8];
             if (a.w && in) {
-                unpack8(load8(a.w, col(c, 0), a.wt), a.wt, wv);
+                unpack8(rw[c], a.wt, wv);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) wv[i] = 1.f;
