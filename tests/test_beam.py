@@ -21,7 +21,7 @@ def _totals(logits, scores, finished, pad):
         lse = m + np.log(np.exp(l - np.where(np.isfinite(m), m, 0)).sum(-1, keepdims=True))
         s = np.where(np.isnan(scores), -INF, scores).astype(np.float64)[..., None]
         t = s + (l - lse)
-    t[np.isnan(t) | ~np.isfinite(s + 0 * t)] = -INF
+    t[np.isnan(t) | np.isneginf(np.broadcast_to(s, t.shape))] = -INF
     if finished is not None:
         for b, w in zip(*np.nonzero(finished)):
             t[b, w] = -INF
