@@ -717,7 +717,7 @@ __device__ __forceinline__ void expand(const LoraArgs &a, const Desc &d, int di,
 
 // grid: tiles x blocks of 16 rows x column blocks of all projections
 template <typename W, int AHEAD>
-__global__ void __launch_bounds__(kThreads, AHEAD == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 3)
 expand_kernel(const __grid_constant__ LoraArgs a) {
     const int mbs = a.T / 16;
     const int sub = blockIdx.x / a.col_blocks, cb = blockIdx.x - sub * a.col_blocks;
@@ -796,7 +796,7 @@ bool allow_smem() {
 
 template <typename X, typename W, int MB>
 bc_status launch(const LoraArgs &a, cudaStream_t s) {
-    // 64 ranks of B ahead where there are that many: a block's steps wait for B otherwise
+    // 32 ranks of B ahead where there are more than 16
     const auto expand = a.R <= 16 ? expand_kernel<W, 1> : expand_kernel<W, kAhead>;
     if (!(a.R <= 16 ? allow_smem<expand_kernel<W, 1>>() : allow_smem<expand_kernel<W, kAhead>>())) return BC_ERR_CUDA;
     shrink_kernel<X, W, MB><<<(unsigned)(a.max_tiles * a.chunks * a.split), kThreads, 0, s>>>(a);
