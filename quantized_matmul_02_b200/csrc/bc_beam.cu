@@ -22,6 +22,8 @@
 // totals agree to about 1e-7.
 #include "bc_internal.cuh"
 
+#include <cooperative_groups.h>
+
 namespace bc {
 namespace {
 
@@ -32,6 +34,7 @@ constexpr int kTile = kThreads * kPer;
 constexpr int64_t kSms = 148;
 constexpr int kMaxOut = 64;
 constexpr int kMaxBeams = 32;
+constexpr int kCluster = 8;
 constexpr int kMaxTiles = 32;                    // per span
 constexpr int64_t kMaxV = 1 << 22;
 constexpr float kMax = 3.402823466e38f;
@@ -168,9 +171,9 @@ __device__ __forceinline__ bool idle(const SelectArgs &a, int64_t r) {
     return (a.finished && a.finished[r]) || isnan(s) || s == -INFINITY;
 }
 
-// grid: rows x spans.  Places u of a row count from the 16-byte boundary at or
+// One span of row r.  Places u of a row count from the 16-byte boundary at or
 // before its first logit (token = u - skip), so that any V reads whole words.
-__global__ void __launch_bounds__(kThreads, 4) beam_span_kernel(const SelectArgs a) {
+__device__ __forceinline__ void scan_span(const SelectArgs &a, const int64_t r, const int sp) {
     __shared__ uint32_t best[kMaxTiles][kThreads];   // ord(maximum) of each group, 0: no logits in it
     __shared__ uint64_t kept[kMaxOut];
     __shared__ int picked[kMaxOut], list[kThreads];  // groups: tile * kThreads + thread
@@ -178,9 +181,6 @@ __global__ void __launch_bounds__(kThreads, 4) beam_span_kernel(const SelectArgs
     __shared__ double dsh[kWarps];
     __shared__ float fsh[kWarps];
     __shared__ int count;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t r = blockIdx.x / a.spans;
-    const int sp = (int)(blockIdx.x - r * a.spans);
     if (idle(a, r)) return;
     const float *row = a.logits + r * a.V;
     const int skip = (int)(reinterpret_cast<uintptr_t>(row) >> 2 & 3);
@@ -420,8 +420,8 @@ __device__ __forceinline__ uint32_t choose(const Key (&k)[P], int n, ChooseShare
 constexpr int kMaxLists = 6 * kThreads;          // a request's spans: at most 4 * kSms + kMaxBeams, or
                                                  // kMaxBeams * (kMaxV / (kMaxTiles * kTile) + 1)
 
-// one block per request
-__global__ void __launch_bounds__(kThreads) beam_join_kernel(const SelectArgs a) {
+// Request b's selection from its spans' lists.
+__device__ __forceinline__ void join_spans(const SelectArgs &a, const int64_t b) {
     __shared__ Key kept[kMaxOut];
     __shared__ int picked[kMaxOut];
     __shared__ double lse[kMaxBeams], score[kMaxBeams];
@@ -429,8 +429,6 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const SelectArgs a)
     __shared__ ChooseShared cs;
     __shared__ int count;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t b = blockIdx.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int w = warp; w < a.beams; w += kWarps) {
         const int64_t r = b * a.beams + w;
         const float sc = a.scores[r];
@@ -556,13 +554,44 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const SelectArgs a)
     }
 }
 
+// grid: rows x spans
+__global__ void __launch_bounds__(kThreads, 4) beam_span_kernel(const SelectArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t r = blockIdx.x / a.spans;
+    scan_span(a, r, (int)(blockIdx.x - r * a.spans));
+}
+// one block per request
+__global__ void __launch_bounds__(kThreads) beam_join_kernel(const SelectArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    join_spans(a, blockIdx.x);
+}
+// Few logits: one launch, a cluster per request; its blocks take the spans in
+// turn, the first one joins them.
+__global__ void __launch_bounds__(kThreads) beam_cluster_kernel(const SelectArgs a) {
+    const int rank = blockIdx.x % kCluster;
+    const int64_t b = blockIdx.x / kCluster;
+    for (int i = rank; i < a.beams * a.spans; i += kCluster) {
+        scan_span(a, b * a.beams + i / a.spans, i % a.spans);
+        __syncthreads();                         // its shared memory is free
+    }
+    cooperative_groups::this_cluster().sync();   // (releases and acquires the lists in global memory)
+    if (rank == 0) join_spans(a, b);
+}
+
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
+// One launch with a cluster per request while a block's share is at most six
+// tiles (a launch costs the host about 3.5 us, more than the longer share) and
+// the clusters fit the GPU at once.
+bool clustered(int64_t batch, int64_t beams, int64_t V) {
+    const int64_t tiles = (V + 3 + kTile - 1) / kTile;
+    return beams <= kCluster && beams * tiles <= 6 * kCluster && batch * kCluster <= 3 * kSms;
+}
 // Spans per row: as many blocks as the GPU holds at once (four per SM), none
 // shorter than one tile; each costs its selection at the end.
-int spans_of(int64_t rows, int64_t V) {
+int spans_of(int64_t batch, int64_t beams, int64_t V) {
     const int64_t tiles = (V + 3 + kTile - 1) / kTile;
-    int64_t want = 4 * kSms / rows;
+    int64_t want = clustered(batch, beams, V) ? kCluster / beams : 4 * kSms / (batch * beams);
     if (want > tiles) want = tiles;
     if (want < 1) want = 1;
     int64_t per = (tiles + want - 1) / want;
@@ -593,7 +622,7 @@ extern "C" {
 
 size_t bc_workspace_size_beam(int64_t batch, int64_t beams, int64_t V, int64_t n_out) {
     if (check_sizes(batch, beams, V, n_out) != BC_OK) return 0;
-    const size_t lists = (size_t)(batch * beams) * spans_of(batch * beams, V);
+    const size_t lists = (size_t)(batch * beams) * spans_of(batch, beams, V);
     return round256(lists * sizeof(SpanOut)) + round256(lists * n_out * 8);
 }
 
@@ -630,7 +659,7 @@ bc_status bc_beam_select(const float *logits, const float *scores, const uint8_t
     a.V = V;
     a.beams = (int)beams;
     a.n_out = (int)n_out;
-    a.spans = spans_of((int64_t)rows, V);
+    a.spans = spans_of(batch, beams, V);
     const int64_t tiles = (V + 3 + kTile - 1) / kTile;
     a.span = (int)((tiles + a.spans - 1) / a.spans * kTile);
     a.eos = eos;
@@ -643,20 +672,31 @@ bc_status bc_beam_select(const float *logits, const float *scores, const uint8_t
     a.token = token;
     a.out_finished = out_finished;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    beam_span_kernel<<<(unsigned)(rows * a.spans), kThreads, 0, s>>>(a);
-    st = cuda_status();
-    if (st != BC_OK) return st;
-    // the second kernel's blocks may start while the first one's finish; they wait for all of it
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)batch);
+    cudaLaunchAttribute at[1];
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, beam_join_kernel, a) != cudaSuccess) {
+    cudaError_t e;
+    if (clustered(batch, beams, V)) {
+        cfg.gridDim = dim3((unsigned)(batch * kCluster));
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = kCluster;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        e = cudaLaunchKernelEx(&cfg, beam_cluster_kernel, a);
+    } else {
+        beam_span_kernel<<<(unsigned)(rows * a.spans), kThreads, 0, s>>>(a);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) {
+            // the second kernel's blocks may start while the first one's finish; they wait for all of it
+            cfg.gridDim = dim3((unsigned)batch);
+            at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            at[0].val.programmaticStreamSerializationAllowed = 1;
+            e = cudaLaunchKernelEx(&cfg, beam_join_kernel, a);
+        }
+    }
+    if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return BC_ERR_CUDA;
     }
