@@ -70,7 +70,6 @@ constexpr float kLog2e = 1.44269504f;
 struct SpanOut {
     double sum;                                  // sum of exp(logit - max)
     float max;                                   // or near it; -inf when nothing is above -inf
-    int count;                                   // keys that follow
 };
 
 // The n largest of the block's keys, P per thread of W 32-bit words (most
@@ -388,12 +387,14 @@ __device__ __forceinline__ void scan_span(const SelectArgs &a, const int64_t r, 
         int rank = 0;
         for (int j = 0; j < n; ++j) rank += kept[j] > kept[tid];
         a.keys[at * n_out + rank] = kept[tid];
+    } else if (tid < n_out) {
+        a.keys[at * n_out + tid] = 0;            // the list is shorter
     }
     if (tid == 0) {
         s = 0;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) s += dsh[i];
-        a.heads[at] = SpanOut{s, bm, n};
+        a.heads[at] = SpanOut{s, bm};
     }
 }
 
@@ -422,23 +423,26 @@ constexpr int kMaxLists = 6 * kThreads;          // a request's spans: at most 4
 
 // Request b's selection from its spans' lists.
 __device__ __forceinline__ void join_spans(const SelectArgs &a, const int64_t b) {
-    __shared__ Key kept[kMaxOut];
+    __shared__ Key kept[kMaxOut], high[kThreads];
     __shared__ int picked[kMaxOut];
     __shared__ double lse[kMaxBeams], score[kMaxBeams];
     __shared__ uint8_t kind[kMaxBeams];          // 0: by its logits, 1: finished, 2: without a score
     __shared__ ChooseShared cs;
     __shared__ int count;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int w = warp; w < a.beams; w += kWarps) {
+    const int tid = threadIdx.x;
+    // eight lanes a beam (32 beams: all at once)
+    {
+        const int w = tid / 8, sub = tid % 8;
         const int64_t r = b * a.beams + w;
-        const float sc = a.scores[r];
+        const bool in = w < a.beams;
+        const float sc = in ? a.scores[r] : -INFINITY;
         const bool dead = isnan(sc) || sc == -INFINITY;
-        const bool fin = a.finished && a.finished[r];
+        const bool fin = in && a.finished && a.finished[r];
         double s = 0;
         float m = -INFINITY;
         if (!dead && !fin) {
             const SpanOut *h = a.heads + r * a.spans;
-            for (int i = lane; i < a.spans; i += 32) {
+            for (int i = sub; i < a.spans; i += 8) {
                 const SpanOut o = h[i];
                 if (o.max > m) {
                     s = s * exp((double)m - (double)o.max) + o.sum;
@@ -447,15 +451,15 @@ __device__ __forceinline__ void join_spans(const SelectArgs &a, const int64_t b)
                     s += o.sum * exp((double)o.max - (double)m);
                 }
             }
-            float bm = m;
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, off));
-            s = m > -INFINITY ? s * exp((double)m - (double)bm) : 0.0;
-            m = bm;
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
         }
-        if (lane == 0) {
+        float bm = m;
+#pragma unroll
+        for (int off = 4; off > 0; off >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, off));
+        s = m > -INFINITY ? s * exp((double)m - (double)bm) : 0.0;
+        m = bm;
+#pragma unroll
+        for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        if (in && sub == 0) {
             kind[w] = dead ? 2 : fin ? 1 : m == -INFINITY ? 2 : 0;
             lse[w] = m > -INFINITY ? (double)m + log(s) : 0.0;
             score[w] = (double)fminf(sc, kMax);
@@ -464,77 +468,138 @@ __device__ __forceinline__ void join_spans(const SelectArgs &a, const int64_t b)
     if (tid == 0) count = 0;
     __syncthreads();
     const uint64_t none = ord64(-INFINITY);
-    // entry `rank` of a list, in descending order; lists are spans, or all of a
-    // beam that does not go by its logits (at its first span)
-    auto entry = [&](int list, int rank) {
-        const int w = list / a.spans, sp = list - w * a.spans;
-        const uint32_t base = (uint32_t)(w * a.V);
-        Key k{0, 0};
-        if (kind[w] == 0) {
-            const int64_t at = (b * a.beams + w) * a.spans + sp;
-            if (rank < a.heads[at].count) {
-                const uint64_t key = a.keys[at * a.n_out + rank];
-                const uint32_t o = (uint32_t)(key >> 32);
-                k.hi = o <= kNegInf ? none : ord64(score[w] + ((double)unord(o) - lse[w]));
-                k.lo = ~(base + ~(uint32_t)key);
-            }
-        } else if (sp == 0 && rank < a.V) {
-            // nothing but -inf, by the lowest tokens; first a finished beam's pad token at its score
-            int64_t v = rank;
-            k.hi = none;
-            if (kind[w] == 1) {
-                if (rank == 0) k.hi = ord64(score[w]);
-                v = rank == 0 ? a.pad : rank - 1 + (rank - 1 >= a.pad);
-            }
-            k.lo = ~(base + (uint32_t)v);
-        }
-        return k;
-    };
-    // the n_out lists with the best first entries hold all that can be chosen
     const int lists = a.beams * a.spans;
-    int n_picked = lists;
-    if (lists * a.n_out > 4 * kThreads) {
-        Key h[kMaxLists / kThreads];
+    // entry `rank` of a list, in descending order; lists are spans, or all of a
+    // beam that does not go by its logits (at its first span).  P at a time:
+    // their loads are on their way together.
+    auto entries = [&](auto &k, auto list, auto rank, int n) {
+        constexpr int P = sizeof(k) / sizeof(k[0]);
+        uint64_t raw[P];
 #pragma unroll
-        for (int i = 0; i < kMaxLists / kThreads; ++i) {
-            const int l = i * kThreads + tid;
-            h[i] = l < lists ? entry(l, 0) : Key{0, 0};
+        for (int i = 0; i < P; ++i) {
+            raw[i] = 0;
+            if (i < n && kind[list(i) / a.spans] == 0)
+                raw[i] = a.keys[(b * lists + list(i)) * a.n_out + rank(i)];
         }
-        const uint32_t mine = choose(h, a.n_out, cs);
 #pragma unroll
-        for (int i = 0; i < kMaxLists / kThreads; ++i)
-            if (mine >> i & 1) picked[atomicAdd(&count, 1)] = i * kThreads + tid;
-        __syncthreads();
-        n_picked = count;
-    }
-    const bool few = n_picked == lists;          // no lists were left out: they are numbered as they are
-    __syncthreads();
-    if (tid == 0) count = 0;
-    const int cands = n_picked * a.n_out;
+        for (int i = 0; i < P; ++i) {
+            k[i] = Key{0, 0};
+            if (i >= n) continue;
+            const int w = list(i) / a.spans, r = rank(i);
+            const uint32_t base = (uint32_t)(w * a.V);
+            if (kind[w] == 0) {
+                const uint32_t o = (uint32_t)(raw[i] >> 32);
+                if (o == 0) continue;                          // the list is shorter
+                k[i].hi = o <= kNegInf ? none : ord64(score[w] + ((double)unord(o) - lse[w]));
+                k[i].lo = ~(base + ~(uint32_t)raw[i]);
+            } else if (list(i) == w * a.spans && r < a.V) {
+                // nothing but -inf, by the lowest tokens; first a finished beam's pad token at its score
+                int64_t v = r;
+                k[i].hi = none;
+                if (kind[w] == 1) {
+                    if (r == 0) k[i].hi = ord64(score[w]);
+                    v = r == 0 ? a.pad : r - 1 + (r - 1 >= a.pad);
+                }
+                k[i].lo = ~(base + (uint32_t)v);
+            }
+        }
+    };
     auto finish = [&](auto &k) {                 // k: this thread's candidates
         const uint32_t mine = choose(k, a.n_out, cs);
 #pragma unroll
         for (int i = 0; i < (int)(sizeof(k) / sizeof(k[0])); ++i)
             if (mine >> i & 1) kept[atomicAdd(&count, 1)] = k[i];
     };
-    auto gather = [&](auto &k) {
-#pragma unroll
-        for (int i = 0; i < (int)(sizeof(k) / sizeof(k[0])); ++i) {
-            const int c = i * kThreads + tid, l = c / a.n_out;
-            k[i] = c < cands ? entry(few ? l : picked[l], c - l * a.n_out) : Key{0, 0};
-        }
+    // candidates c0, c0 + kThreads, ... of the lists' n_out entries each
+    auto candidates = [&](auto &k, int cands, auto list) {
+        entries(k, [&](int i) { return list((tid + i * kThreads) / a.n_out); },
+                [&](int i) { return (tid + i * kThreads) % a.n_out; }, (cands - tid + kThreads - 1) / kThreads);
     };
-    if (cands <= kThreads) {
+    auto itself = [](int l) { return l; };
+    bool done = lists * a.n_out <= 4 * kThreads;
+    if (lists * a.n_out <= kThreads) {
         Key k[1];
-        gather(k);
+        candidates(k, lists * a.n_out, itself);
         finish(k);
-    } else if (cands <= 4 * kThreads) {
+    } else if (done) {
         Key k[4];
-        gather(k);
+        candidates(k, lists * a.n_out, itself);
         finish(k);
     } else {
+        // Many.  A bar that n_out entries reach: `depth` entries of each of the
+        // n_out / depth lists whose depth-th is best.  Entries that reach it are
+        // few, unless equal or in a few lists.
+        const int depth = min(max(a.n_out / 8, 1), 8), need = (a.n_out + depth - 1) / depth;
+        Key bar{0, 0};
+        auto lowest = [&](auto &h) {
+            // (a thread's lists lie kThreads apart)
+            entries(h, [&](int i) { return i * kThreads + tid; }, [&](int) { return depth - 1; },
+                    (lists - tid + kThreads - 1) / kThreads);
+            const uint32_t mine = choose(h, need, cs);
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(h) / sizeof(h[0])); ++i)
+                if (mine >> i & 1) kept[atomicAdd(&count, 1)] = h[i];
+            __syncthreads();
+            const int n = count;
+            if (n == need) {
+                bar = kept[0];
+                for (int i = 1; i < n; ++i)
+                    if (above(bar, kept[i])) bar = kept[i];
+            }
+            __syncthreads();
+            if (tid == 0) count = 0;
+            __syncthreads();
+        };
+        if (lists <= kThreads) {
+            Key h[1];
+            lowest(h);
+        } else {
+            Key h[kMaxLists / kThreads];
+            lowest(h);
+        }
+        if (bar.hi) {
+            for (int l = tid; l < lists; l += kThreads)
+                for (int r0 = 0; r0 < a.n_out; r0 += 8) {
+                    Key k[8];
+                    entries(k, [&](int) { return l; }, [&](int i) { return r0 + i; }, a.n_out - r0);
+                    bool more = false;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        more = k[i].hi && !above(bar, k[i]);   // entries descend: false from the first on
+                        if (more) {
+                            const int to = atomicAdd(&count, 1);
+                            if (to < kThreads) high[to] = k[i];
+                        }
+                    }
+                    if (!more || count > kThreads) break;
+                }
+            __syncthreads();
+            const int n = count;
+            __syncthreads();
+            if (tid == 0) count = 0;
+            if (n <= kThreads) {
+                Key k[1] = {tid < n ? high[tid] : Key{0, 0}};
+                finish(k);
+                done = true;
+            }
+        }
+    }
+    if (!done) {
+        // the n_out lists with the best first entries hold all that can be chosen
+        __syncthreads();
+        Key h[kMaxLists / kThreads];
+        entries(h, [&](int i) { return i * kThreads + tid; }, [](int) { return 0; },
+                (lists - tid + kThreads - 1) / kThreads);
+        const uint32_t mine = choose(h, a.n_out, cs);
+#pragma unroll
+        for (int i = 0; i < kMaxLists / kThreads; ++i)
+            if (mine >> i & 1) picked[atomicAdd(&count, 1)] = i * kThreads + tid;
+        __syncthreads();
+        const int n = count;
+        __syncthreads();
+        if (tid == 0) count = 0;
         Key k[kMaxOut * kMaxOut / kThreads];
-        gather(k);
+        candidates(k, n * a.n_out, [&](int l) { return picked[l]; });
         finish(k);
     }
     __syncthreads();
@@ -580,12 +645,12 @@ __global__ void __launch_bounds__(kThreads) beam_cluster_kernel(const SelectArgs
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// One launch with a cluster per request while a block's share is at most six
+// One launch with a cluster per request while a block's share is at most ten
 // tiles (a launch costs the host about 3.5 us, more than the longer share) and
 // the clusters fit the GPU at once.
 bool clustered(int64_t batch, int64_t beams, int64_t V) {
     const int64_t tiles = (V + 3 + kTile - 1) / kTile;
-    return beams <= kCluster && beams * tiles <= 6 * kCluster && batch * kCluster <= 3 * kSms;
+    return beams <= kCluster && beams * tiles <= 10 * kCluster && batch * kCluster <= 3 * kSms;
 }
 // Spans per row: as many blocks as the GPU holds at once (four per SM), none
 // shorter than one tile; each costs its selection at the end.
