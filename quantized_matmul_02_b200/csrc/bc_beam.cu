@@ -558,21 +558,25 @@ __device__ __forceinline__ void join_spans(const SelectArgs &a, const int64_t b)
             lowest(h);
         }
         if (bar.hi) {
-            for (int l = tid; l < lists; l += kThreads)
-                for (int r0 = 0; r0 < a.n_out; r0 += 8) {
+            const int eighths = (a.n_out + 7) / 8;             // a list's entries, eight at a time
+            for (int c0 = tid; c0 < lists * eighths; c0 += 4 * kThreads) {
+                auto list = [&](int i) { return (c0 + i * kThreads) / eighths; };
+                auto rank = [&](int i) { return (c0 + i * kThreads) % eighths * 8; };
+                Key f[4];
+                entries(f, list, rank, (lists * eighths - c0 + kThreads - 1) / kThreads);
+                for (int e = 0; e < 4; ++e) {
+                    const Key first = e == 0 ? f[0] : e == 1 ? f[1] : e == 2 ? f[2] : f[3];
+                    if (!first.hi || above(bar, first)) continue;  // entries descend
                     Key k[8];
-                    entries(k, [&](int) { return l; }, [&](int i) { return r0 + i; }, a.n_out - r0);
-                    bool more = false;
+                    entries(k, [&](int) { return list(e); }, [&](int i) { return rank(e) + i; }, a.n_out - rank(e));
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        more = k[i].hi && !above(bar, k[i]);   // entries descend: false from the first on
-                        if (more) {
+                    for (int i = 0; i < 8; ++i)
+                        if (k[i].hi && !above(bar, k[i])) {
                             const int to = atomicAdd(&count, 1);
                             if (to < kThreads) high[to] = k[i];
                         }
-                    }
-                    if (!more || count > kThreads) break;
                 }
+            }
             __syncthreads();
             const int n = count;
             __syncthreads();
