@@ -13,6 +13,10 @@
 // second launch joins the spans of each beam and selects over a request's
 // beams.  HBM bound: 4 bytes per logit against about seven operations.
 //
+// Measured, on the GPU alone: 256 rows of 151936 logits, 16 candidates: 33 us,
+// 4.7 TB/s (lists of candidates above a running floor instead of the maxima:
+// 57 us, half of it their appending; rank counts: 163).  4 rows of 32003: 10 us.
+//
 // Keys (value, place) are all distinct, so the result does not depend on the
 // order in which candidates are collected.
 //
@@ -650,14 +654,15 @@ __global__ void __launch_bounds__(kThreads) beam_cluster_kernel(const SelectArgs
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 // One launch with a cluster per request while a block's share is at most ten
-// tiles (a launch costs the host about 3.5 us, more than the longer share) and
-// the clusters fit the GPU at once.
+// tiles and the clusters fit the GPU at once: 4 rows of 32003 take 10 us on the
+// GPU either way, and the host is busy for 17 us a call instead of 21.
 bool clustered(int64_t batch, int64_t beams, int64_t V) {
     const int64_t tiles = (V + 3 + kTile - 1) / kTile;
     return beams <= kCluster && beams * tiles <= 10 * kCluster && batch * kCluster <= 3 * kSms;
 }
-// Spans per row: as many blocks as the GPU holds at once (four per SM), none
-// shorter than one tile; each costs its selection at the end.
+// Spans per row: as many blocks as the GPU holds at once (four per SM: 256 rows
+// 34 us; half as many again 40, twice 42), none shorter than one tile; each
+// costs its selection at the end.
 int spans_of(int64_t batch, int64_t beams, int64_t V) {
     const int64_t tiles = (V + 3 + kTile - 1) / kTile;
     int64_t want = clustered(batch, beams, V) ? kCluster / beams : 4 * kSms / (batch * beams);

@@ -8,14 +8,22 @@
 // are cut into tiles.  shrink_kernel forms c A x, a block per (tile, 32 ranks of
 // the projections that read the same x, part of K), and leaves it in scratch,
 // in the order of expand_kernel's fragments.  expand_kernel joins the parts
-// and adds B v, a block per (16 rows, columns).  x, A, B, v and y go between global memory and
-// matrix fragments directly: the order of the contraction index is free, so a
-// lane takes 16-byte pieces along it, and y's columns are dealt to the
-// fragments so that lanes side by side hold whole sectors.
+// and adds B v, a block per (16 rows, columns).  x, A, B and v go from global
+// memory to matrix fragments directly: the order of the contraction index is
+// free, so a lane takes 16-byte pieces along it, and y's columns are dealt to
+// the fragments so that lanes side by side hold whole sectors.
 //
 // What bounds it: the bytes of y (fp32, read and written) and x for prompts,
-// the bytes of the adapters for single tokens; 2 R (K + N) operations a row
-// are small beside them up to R = 128.
+// the bytes of the adapters for single tokens.  2 R (K + N) operations a row
+// are few beside them (16 per byte of y at R = 64), and tiles have 16 or 32
+// rows, so the products run on mma.sync from registers.  Above R = 64 with
+// many rows, B's trips from L2 (once per 16 rows) and the tensor cores bind.
+//
+// Measured, on the GPU alone: 4100 rows of bf16, 4096 -> 2 x 12288, rank 16:
+// 135 us, 6.3 TB/s of the 847 MB that it must move (one fused kernel of
+// clusters that exchange v through distributed shared memory: 205 us; y read
+// and written in half sectors: 201 us).  64 rows over 48 adapters of rank 32,
+// 4096 -> 4096 + 2 x 1024: 18 us of 9.3.  One row, 896 -> 896 + 2 x 128: 9 us.
 //
 // Precision: fp32 throughout.  Products of 16-bit values are exact in the
 // tensor cores (of one type, or in tf32, which holds bf16 and fp16 exactly).
@@ -38,10 +46,12 @@ constexpr int kMaxSegments = 4096;
 constexpr int kMaxRank = 128;
 constexpr int kGroupRows = 256;        // up to here rows are ordered by adapter
 constexpr int kChunk = 32;             // ranks per shrink block
-constexpr int kFew = 2;                // rows up to here: plain products instead of fragments
+// Rows up to here: plain products instead of fragments (64 decode rows over 48
+// adapters: 25 us with them, 31 without; 4 rows spill registers, 27).
+constexpr int kFew = 2;
 constexpr int kMaxSplit = 8;           // parts of K
 constexpr int kStep = kWarps * 32;     // columns an expand block takes at a time
-constexpr int kMaxSteps = 6;          // such steps per block
+constexpr int kMaxSteps = 6;           // such steps per block (4100 rows: 6 135 us, 12 136, 16 142)
 constexpr int kAhead = 2;              // 16-rank pieces of B on their way, for more than 16 ranks
 constexpr int kStages = 3;             // of which y is on its way
 constexpr int kRing = kWarps * kStages * 4 * 32;   // 16-byte pieces of y in shared memory
@@ -716,6 +726,7 @@ __device__ __forceinline__ void expand(const LoraArgs &a, const Desc &d, int di,
 }
 
 // grid: tiles x blocks of 16 rows x column blocks of all projections
+// (three blocks per SM: 4100 rows take 135 us, with two 152, with four 141)
 template <typename W, int AHEAD>
 __global__ void __launch_bounds__(kThreads, 3)
 expand_kernel(const __grid_constant__ LoraArgs a) {
@@ -734,8 +745,9 @@ expand_kernel(const __grid_constant__ LoraArgs a) {
         expand<W, false, AHEAD>(a, d, di, ti, mb, mbs, cb - d.first_block, tile);
 }
 
-// Tile height: 16 rows while rows are few or segments short, else 32; fp32
-// rows take 16 (two pieces of 32 would not fit the registers).
+// Tile height: 16 rows while rows are few or segments short, else 32, which
+// halves A's trips from L2; fp32 rows take 16 (two pieces of 32 rows would not
+// fit the registers: 187 for a thread).
 int tile_rows(int64_t M, int64_t S, bool f32) { return f32 || M <= kGroupRows || M / S <= 16 ? 16 : 32; }
 // At most this many tiles: full ones, and a ragged one per segment (or adapter).
 int64_t most_tiles(int64_t M, int64_t S, int64_t adapters, int64_t T) {
@@ -754,7 +766,7 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 // 32-rank chunks of a launch (neighbours that read the same x share a pass
 // over it), and the parts of K: about two blocks per SM, each with 1024 of K
-// or more.
+// or more (64 decode rows at K = 4096: 21 us; three blocks per SM 25).
 struct Shape {
     int64_t T, tiles;
     int chunks, split;
@@ -796,7 +808,7 @@ bool allow_smem() {
 
 template <typename X, typename W, int MB>
 bc_status launch(const LoraArgs &a, cudaStream_t s) {
-    // 32 ranks of B ahead where there are more than 16
+    // 32 ranks of B ahead where there are more than 16 (777 rows, rank 128: 19.5 us, with 16 23)
     const auto expand = a.R <= 16 ? expand_kernel<W, 1> : expand_kernel<W, kAhead>;
     if (!(a.R <= 16 ? allow_smem<expand_kernel<W, 1>>() : allow_smem<expand_kernel<W, kAhead>>())) return BC_ERR_CUDA;
     shrink_kernel<X, W, MB><<<(unsigned)(a.max_tiles * a.chunks * a.split), kThreads, 0, s>>>(a);
