@@ -338,7 +338,8 @@ BC_API size_t bc_workspace_size_argmax(int64_t M, int64_t N, int64_t K, bc_mode 
  *   out       [M][D] out_dtype, device, written; may be x itself when the
  *             types agree.  What is written may overlap nothing else.
  *   eps       above 0
- * Any M up to 2^24 and D up to 2^24.  Pointers need the alignment of their
+ * Values up to about 1e18 (their squares are summed in fp32).  Any M up to
+ * 2^24 and D up to 2^24.  Pointers need the alignment of their
  * element type; rows are read in 16-byte pieces when every pointer is 16-byte
  * aligned and D is a multiple of 8.
  */
@@ -490,7 +491,7 @@ BC_API size_t bc_workspace_size_matmul_beam(int64_t batch, int64_t beams, int64_
  * ([layers][batch * beams][...]).
  */
 typedef struct bc_beam_state {
-    void *data;               /* device, any alignment (16 bytes is fastest) */
+    void *data;               /* device, any alignment */
     int64_t rows;
     int64_t row_bytes;
     int64_t row_stride;
@@ -506,9 +507,9 @@ typedef struct bc_beam_state {
  *   states   HOST array of `count` states (read before return); they may not
  *            overlap one another or `parent`
  *   parent   int32, device: parent[i * parent_stride + w] (parent_stride >= beams)
- * beams <= 32, batch <= 65535; rows * row_bytes of one state below 2^31 of
- * the widest pieces (16, 8, 4, 2 or 1 bytes) that its address, lengths and
- * strides are multiples of.
+ * beams <= 32, batch <= 65535; one state below 2^31 pieces: rows * row_bytes
+ * by 16 bytes, or, of short runs whose address, lengths and strides are not
+ * multiples of 16, by the widest of 8, 4, 2 or 1 that they are multiples of.
  */
 BC_API bc_status bc_beam_reorder(const bc_beam_state *states, int count,
                                  const int32_t *parent, int64_t parent_stride,

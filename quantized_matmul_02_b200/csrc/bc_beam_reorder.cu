@@ -18,11 +18,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxStates = 64;         // per launch (kernel parameters)
 constexpr int kMaxBeams = 32;
+constexpr int kTileBytes = 32768;      // of all beams of a block that moves unaligned bytes
 
 struct State {
     uint8_t *data;
     int64_t row_stride, beam_stride;
-    uint32_t rows, units;              // units of `vec` bytes per row
+    int64_t row_bytes;
+    uint32_t rows, units;              // units of `vec` bytes per row, or tiles of a long unaligned one
     int vec;
 };
 struct ReorderArgs {
@@ -79,11 +81,93 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
     }
 }
 
+// Long runs that are not multiples of 16 bytes apart: through shared memory,
+// so that both sides move 16 aligned bytes at a time.  A block owns `tile`
+// bytes of one run, of all beams of a request; it loads the parents' in place
+// (with the source's phase), waits, and stores to each beam with its own.
+// grid (tiles x rows, batch, states)
+template <int WMAX>
+__global__ void __launch_bounds__(kThreads) reorder_bytes_kernel(const __grid_constant__ ReorderArgs a) {
+    constexpr int kTile = kTileBytes / WMAX, kSlot = kTile + 32, kPieces = kTile / 16 + 1;
+    __shared__ __align__(16) uint8_t buf[WMAX * kSlot];
+    __shared__ int src[kMaxBeams];
+    __shared__ int list[kMaxBeams], n_moved;       // beams that move
+    const State &st = a.st[blockIdx.z];
+    if (blockIdx.x >= st.rows * st.units) return;
+    if (threadIdx.x < 32) {
+        const int w = threadIdx.x;
+        int p = w;
+        if (w < a.beams) {
+            p = a.parent[blockIdx.y * a.parent_stride + w];
+            if (p < 0 || p >= a.beams) p = w;          // no such beam: stays as it is
+        }
+        src[w] = p;
+        const uint32_t m = __ballot_sync(0xffffffffu, p != w);
+        if (p != w) list[__popc(m & ((1u << w) - 1))] = w;
+        if (w == 0) n_moved = __popc(m);
+    }
+    __syncthreads();
+    if (n_moved == 0) return;
+    const uint32_t row = blockIdx.x / st.units, tile = blockIdx.x - row * st.units;
+    const int64_t c0 = (int64_t)tile * kTile;
+    const int n = (int)min((int64_t)kTile, st.row_bytes - c0);
+    uint8_t *base = st.data + (int64_t)blockIdx.y * a.beams * st.beam_stride + row * st.row_stride + c0;
+    for (int i = threadIdx.x; i < n_moved * kPieces; i += kThreads) {
+        const int s = i / kPieces, o = (i - s * kPieces) * 16;
+        const uint8_t *from = base + src[list[s]] * st.beam_stride;
+        const int phase = (int)(reinterpret_cast<uintptr_t>(from) & 15);
+        uint8_t *to = buf + s * kSlot + o;
+        const int j = o - phase;                       // the piece's first byte, in the tile
+        if (j >= 0 && j + 16 <= n) {
+            *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from + j);
+        } else {
+            for (int e = 0; e < 16; ++e)
+                if (j + e >= 0 && j + e < n) to[e] = from[j + e];
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_moved * kPieces; i += kThreads) {
+        const int s = i / kPieces, o = (i - s * kPieces) * 16;
+        uint8_t *to = base + list[s] * st.beam_stride;
+        const int j = o - (int)(reinterpret_cast<uintptr_t>(to) & 15);
+        const uint8_t *from = buf + s * kSlot +
+            (reinterpret_cast<uintptr_t>(base + src[list[s]] * st.beam_stride) & 15);
+        if (j >= 0 && j + 16 <= n) {
+            // 16 bytes at any place: two aligned pieces, shifted
+            const uint32_t q = (uint32_t)(from + j - buf), words = q >> 2 & 3, bits = (q & 3) * 8;
+            const uint4 lo = *reinterpret_cast<const uint4 *>(buf + (q & ~15u));
+            const uint4 hi = *reinterpret_cast<const uint4 *>(buf + (q & ~15u) + 16);
+            uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            if (words & 1)
+#pragma unroll
+                for (int e = 0; e < 7; ++e) v[e] = v[e + 1];
+            if (words & 2)
+#pragma unroll
+                for (int e = 0; e < 6; ++e) v[e] = v[e + 2];
+            *reinterpret_cast<uint4 *>(to + j) =
+                make_uint4(__funnelshift_r(v[0], v[1], bits), __funnelshift_r(v[1], v[2], bits),
+                           __funnelshift_r(v[2], v[3], bits), __funnelshift_r(v[3], v[4], bits));
+        } else {
+            for (int e = 0; e < 16; ++e)
+                if (j + e >= 0 && j + e < n) to[j + e] = from[j + e];
+        }
+    }
+}
+
 // Widest access that the address, the length and the strides of a state allow.
 int vec_of(const bc_beam_state &d) {
     const uint64_t bits = reinterpret_cast<uintptr_t>(d.data) | (uint64_t)d.row_bytes |
                           (uint64_t)d.beam_stride | (d.rows > 1 ? (uint64_t)d.row_stride : 0);
     return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+}
+
+// Whether a state goes through shared memory: from 512 bytes a run, where its
+// pieces would be narrower than 16.
+bool by_bytes(const bc_beam_state &d) { return d.row_bytes >= 512 && vec_of(d) < 16; }
+// Pieces (of the widest access, or a block's tile) of a run.
+uint64_t units_of(const bc_beam_state &d, int64_t beams) {
+    const int64_t tile = kTileBytes / (beams <= 4 ? 4 : beams <= 8 ? 8 : beams <= 16 ? 16 : 32);
+    return by_bytes(d) ? (uint64_t)((d.row_bytes + tile - 1) / tile) : (uint64_t)d.row_bytes / vec_of(d);
 }
 
 }  // namespace
@@ -114,8 +198,7 @@ extern "C" bc_status bc_beam_reorder(const bc_beam_state *states, int count, con
             const bool rows_outside = (unsigned __int128)d.row_stride >= all;
             if (!beams_outside && !rows_outside) return BC_ERR_INVALID_ARG;
         }
-        const int vec = vec_of(d);
-        if ((unsigned __int128)(d.row_bytes / vec) * d.rows >= (1ull << 31)) return BC_ERR_UNSUPPORTED;
+        if ((unsigned __int128)units_of(d, beams) * d.rows >= (1ull << 31)) return BC_ERR_UNSUPPORTED;
         for (int j = 0; j < i; ++j)
             if (states[j].data == d.data) return BC_ERR_INVALID_ARG;   // would be moved twice
         const unsigned __int128 end = (unsigned __int128)reinterpret_cast<uintptr_t>(d.data) +
@@ -130,24 +213,33 @@ extern "C" bc_status bc_beam_reorder(const bc_beam_state *states, int count, con
     a.parent = parent;
     a.parent_stride = parent_stride;
     a.beams = (int)beams;
-    for (int i = 0; i < count; i += kMaxStates) {
-        const int n = count - i < kMaxStates ? count - i : kMaxStates;
-        uint64_t most = 0;
-        for (int j = 0; j < n; ++j) {
-            const bc_beam_state &d = states[i + j];
-            const int vec = vec_of(d);
-            const uint64_t units = (uint64_t)d.row_bytes / vec;
-            a.st[j] = State{static_cast<uint8_t *>(d.data), d.rows > 1 ? d.row_stride : 0, d.beam_stride,
-                            (uint32_t)d.rows, (uint32_t)units, vec};
-            if (units * d.rows > most) most = units * d.rows;
+    for (int bytes = 0; bytes < 2; ++bytes)                // aligned (or short) runs, then the others
+        for (int i = 0; i < count;) {
+            int n = 0;
+            uint64_t most = 0;
+            for (; i < count && n < kMaxStates; ++i) {
+                const bc_beam_state &d = states[i];
+                if (by_bytes(d) != (bytes == 1)) continue;
+                const uint64_t units = units_of(d, beams);
+                a.st[n++] = State{static_cast<uint8_t *>(d.data), d.rows > 1 ? d.row_stride : 0, d.beam_stride,
+                                  d.row_bytes, (uint32_t)d.rows, (uint32_t)units, vec_of(d)};
+                if (units * d.rows > most) most = units * d.rows;
+            }
+            if (n == 0) continue;
+            const dim3 grid((unsigned)(bytes ? most : (most + kThreads - 1) / kThreads), (unsigned)batch, (unsigned)n);
+            if (bytes) {
+                if (beams <= 4) reorder_bytes_kernel<4><<<grid, kThreads, 0, s>>>(a);
+                else if (beams <= 8) reorder_bytes_kernel<8><<<grid, kThreads, 0, s>>>(a);
+                else if (beams <= 16) reorder_bytes_kernel<16><<<grid, kThreads, 0, s>>>(a);
+                else reorder_bytes_kernel<32><<<grid, kThreads, 0, s>>>(a);
+            } else {
+                if (beams <= 4) reorder_kernel<4><<<grid, kThreads, 0, s>>>(a);
+                else if (beams <= 8) reorder_kernel<8><<<grid, kThreads, 0, s>>>(a);
+                else if (beams <= 16) reorder_kernel<16><<<grid, kThreads, 0, s>>>(a);
+                else reorder_kernel<32><<<grid, kThreads, 0, s>>>(a);
+            }
+            const bc_status st = cuda_status();
+            if (st != BC_OK) return st;
         }
-        const dim3 grid((unsigned)((most + kThreads - 1) / kThreads), (unsigned)batch, (unsigned)n);
-        if (beams <= 4) reorder_kernel<4><<<grid, kThreads, 0, s>>>(a);
-        else if (beams <= 8) reorder_kernel<8><<<grid, kThreads, 0, s>>>(a);
-        else if (beams <= 16) reorder_kernel<16><<<grid, kThreads, 0, s>>>(a);
-        else reorder_kernel<32><<<grid, kThreads, 0, s>>>(a);
-        const bc_status st = cuda_status();
-        if (st != BC_OK) return st;
-    }
     return BC_OK;
 }

@@ -863,7 +863,7 @@ bool sizes_ok(const bc_lora_desc *descs, int count, int64_t M, int64_t R, int64_
             cols += (descs[i + j].N + kStep - 1) / kStep;
         }
         // blocks of one launch
-        if (tiles * cols >= (int64_t)1 << 31) return false;
+        if (2 * tiles * cols >= (int64_t)1 << 31) return false;        // (32-row tiles round up twice)
         if (tiles * n * ((R + kChunk - 1) / kChunk) * kMaxSplit >= (int64_t)1 << 31) return false;
     }
     *st = BC_OK;

@@ -228,7 +228,10 @@ def test_select_rejects_on_host():
 @pytest.mark.parametrize("beams", [1, 2, 4, 5, 8, 13, 32])
 @pytest.mark.parametrize("shape,cut,dt", [((1,), None, torch.int32), ((3, 40, 16), 25, torch.bfloat16),
                                           ((5, 33), 17, torch.uint8), ((2, 1000, 8), 999, torch.float16),
-                                          ((77,), None, torch.uint8), ((4, 6), 5, torch.int16)])
+                                          ((77,), None, torch.uint8), ((4, 6), 5, torch.int16),
+                                          ((2, 1501), 1499, torch.uint8), ((9001,), None, torch.uint8),
+                                          ((3, 5003), 5001, torch.int16), ((1, 20003), 20000, torch.uint8),
+                                          ((2, 515), 513, torch.int32), ((512,), None, torch.uint8)])
 def test_reorder(cuda_lib, beams, shape, cut, dt):
     batch = 3
     g = torch.Generator().manual_seed(beams)
@@ -282,7 +285,7 @@ def test_reorder_rejects_on_host():
     assert call(state=(None, 4, 64, 128, 1024)) == 1 and call(state=(FAKE, 0, 64, 128, 1024)) == 1
     assert call(state=(FAKE, 4, 64, 32, 1024)) == 1          # runs overlap
     assert call(state=(FAKE, 4, 64, 128, 256)) == 1          # beams overlap
-    assert call(state=(FAKE, 1, 1 << 33, 0, (1 << 33) + 1)) == 2
+    assert call(state=(FAKE, 1 << 31, 4, 4, 1 << 34), parent=1 << 45) == 2 and call(state=(FAKE, 1, 1 << 47, 0, 1 << 47)) == 2
     assert call(parent=FAKE + 64) == 1                        # parent inside the state
     assert call(count=2, more=[(FAKE, 1, 64, 0, 64)]) == 1   # the same state twice
     with pytest.raises(ValueError):
