@@ -507,9 +507,9 @@ typedef struct bc_beam_state {
  *   states   HOST array of `count` states (read before return); they may not
  *            overlap one another or `parent`
  *   parent   int32, device: parent[i * parent_stride + w] (parent_stride >= beams)
- * beams <= 32, batch <= 65535; one state below 2^31 pieces: rows * row_bytes
- * by 16 bytes, or, of short runs whose address, lengths and strides are not
- * multiples of 16, by the widest of 8, 4, 2 or 1 that they are multiples of.
+ * beams <= 32, batch <= 65535; rows * row_bytes of one state below 2^31
+ * pieces, of the widest of 16, 8, 4, 2 or 1 bytes that its address, lengths
+ * and strides are multiples of.
  */
 BC_API bc_status bc_beam_reorder(const bc_beam_state *states, int count,
                                  const int32_t *parent, int64_t parent_stride,
