@@ -81,9 +81,10 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
     }
 }
 
-// Long runs at odd places: through shared memory, so that both sides move 16 aligned bytes at a time.  A block owns `tile`
-// bytes of one run, of all beams of a request; it loads the parents' in place
-// (with the source's phase), waits, and stores to each beam with its own.
+// Long runs at odd places: through shared memory, so that both sides move 16
+// aligned bytes at a time.  A block owns a tile of one run, of all beams of a
+// request; it loads the parents' (with the source's phase), waits, and stores
+// to each beam with its own.
 // grid (tiles x rows, batch, states)
 template <int WMAX>
 __global__ void __launch_bounds__(kThreads) reorder_bytes_kernel(const __grid_constant__ ReorderArgs a) {

@@ -61,6 +61,29 @@ def test_norm(cuda_lib, M, D, xt, rt, wt, ot):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("xt,rt,wt,ot", [(F32, F32, F16, F32), (BF16, BF16, BF16, BF16), (F16, None, None, F32)])
+@pytest.mark.parametrize("M,D", [(3001, 264), (2400, 704), (1500, 1344), (700, 4088)])
+def test_norm_of_many_rows(cuda_lib, M, D, xt, rt, wt, ot):
+    """Enough rows that a block takes several."""
+    x, r, w = _inputs(M, D, xt, rt, wt, D)
+    h, v = _formula(x, r, w)
+    res = r if r is None else r.clone()
+    _near(cuda_lib.add_rmsnorm(x, w, EPS, residual=res, out_dtype=ot), v, _rel(D) + (_step(ot) if ot != F32 else 0), 2.0 ** -25)
+    if r is not None:
+        _near(res, h, 2.0 ** -24 + _step(r.dtype), 2.0 ** -25)
+    if xt == ot:
+        cuda_lib.add_rmsnorm(x, w, EPS, residual=r, out=x)
+        _near(x, v, _rel(D) + (_step(ot) if ot != F32 else 0), 2.0 ** -25)
+
+
+@pytest.mark.gpu
+def test_norm_q8_of_many_rows(cuda_lib):
+    x, r, w = _inputs(1600, 1344, F32, BF16, F16, 9)
+    _, v = _formula(x, r, w)
+    _check_q8(cuda_lib.add_rmsnorm_q8(x, w, EPS, residual=r), v, _rel(1344))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("shift", [0, 1, 2, 4])
 def test_norm_of_unaligned_views(cuda_lib, shift):
     """Addresses that only have their element's alignment."""
