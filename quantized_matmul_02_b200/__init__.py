@@ -513,13 +513,15 @@ def make_lora_descs(items: Sequence[tuple]) -> LoraDescs:
             _same_device(what, dev, x)
             xp, seen = x.data_ptr(), x
         N = y.shape[-1]
-        if A.dtype != wt or A.shape != (n, R, K):
+        if A.dtype is not wt or A.shape != (n, R, K):
             _bad(what, "A", A, (n, R, K), wt)
-        if B.dtype != wt or B.shape != (n, N, R):
+        if B.dtype is not wt or B.shape != (n, N, R):
             _bad(what, "B", B, (n, N, R), wt)
-        if y.dtype != _F32 or y.shape != (M, N):
+        if y.dtype is not _F32 or y.shape != (M, N):
             _bad(what, "y", y, (M, N), _F32)
-        _same_device(what, dev, A, B, y)
+        if not (A.get_device() == B.get_device() == y.get_device() == dev and A.is_contiguous()
+                and B.is_contiguous() and y.is_contiguous()):
+            _same_device(what, dev, A, B, y)
         fields += (xp, A.data_ptr(), B.data_ptr(), y.data_ptr(), N, K)
     d = LoraDescs()
     d.M, d.n_adapters, d.R, d.count, d.device = M, n, R, len(items), dev
@@ -551,10 +553,9 @@ def lora_add_batched(descs: LoraDescs, seg_start: torch.Tensor, seg_adapter: tor
         _bad(what, "ranks", ranks, (n,), _I32)
     if scaling is not None and (scaling.dtype != _F32 or scaling.shape != (n,)):
         _bad(what, "scaling", scaling, (n,), _F32)
-    dev = _one_device(what, seg_start, seg_adapter, ranks, scaling, workspace)
-    if dev != descs.device:
-        raise ValueError(f"{what}: all tensors must be on one CUDA device")
-    other = _elsewhere(what, dev, stream)
+    dev = descs.device
+    _same_device(what, dev, seg_start, seg_adapter, ranks, scaling, workspace)
+    other = None if stream is None and dev == _current_device() else _elsewhere(what, dev, stream)
     if other is not None:
         with other:
             return lora_add_batched(descs, seg_start, seg_adapter, ranks, scaling, workspace)
@@ -607,12 +608,14 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int,
         raise ValueError(f"{what}: logits must be [batch * beams][V], scores [batch][beams]")
     batch, beams = scores.shape
     V = logits.shape[1]
-    _want(what, "logits", logits, (batch * beams, V), _F32)
-    _want(what, "scores", scores, (batch, beams), _F32)
+    if logits.dtype is not _F32 or logits.shape[0] != batch * beams:
+        _bad(what, "logits", logits, (batch * beams, V), _F32)
+    if scores.dtype is not _F32:
+        _bad(what, "scores", scores, (batch, beams), _F32)
     if finished is not None:
         _want(what, "finished", finished, (batch, beams), _U8, torch.bool)
     dev = _one_device(what, logits, scores, finished, workspace, *(out or ()))
-    other = _elsewhere(what, dev, stream)
+    other = None if stream is None and dev == _current_device() else _elsewhere(what, dev, stream)
     if other is not None:
         with other:
             return beam_select(logits, scores, n_out, finished, eos, pad, out, workspace)
