@@ -409,6 +409,24 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) xrow[mb][h] = x_row(min(mb * 16 + g + h * 8, n_rows - 1)) + t * 8;
         float acc[MB][NB][4] = {};
+        // The tensor cores cut off what lies below an accumulator's last bit, half
+        // of it a product on average, so long sums are taken in parts: the warp's
+        // own place in red[] holds them (fp32 x, K = 12288: y 3.0e-7 off, in one
+        // sum 6.6e-7).
+        bool parts = false;
+        auto flush = [&] {
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    float4 &r = red[warp * (T * kChunk / 4) + (mb * NB + b) * 32 + lane];
+                    const float4 s = parts ? r : make_float4(0.f, 0.f, 0.f, 0.f);
+                    r = make_float4(s.x + acc[mb][b][0], s.y + acc[mb][b][1], s.z + acc[mb][b][2], s.w + acc[mb][b][3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[mb][b][e] = 0.f;
+                }
+            parts = true;
+        };
         auto run = [&](auto blocks_c) {
             constexpr int L = decltype(blocks_c)::value;       // blocks of ranks
             auto load = [&](int u, uint4 (&wa)[L], uint4 (&xa)[MB][2][kQ]) {
@@ -470,7 +488,12 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
             const int step = a.split * kWarps, units = K / 32;
             int u = part * kWarps + warp;
             if (u < units) load(u, wa[0], xa[0]);
-            for (; u < units; u += 2 * step) {
+            for (int done = 0; u < units; u += 2 * step) {
+                if (done == (kF32 ? 1 : kBf16 ? 4 : 2)) {      // after 16 products
+                    flush();
+                    done = 0;
+                }
+                ++done;
                 if (u + step < units) load(u + step, wa[1], xa[1]);
                 multiply(wa[0], xa[0]);
                 if (u + step < units) {
@@ -485,12 +508,7 @@ shrink_kernel(const __grid_constant__ LoraArgs a) {
         else if (nb == 2) run(std::integral_constant<int, 2>());
         else run(std::integral_constant<int, 1>());
         // the block's sum over its warps, in fragment order
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-                red[warp * kQuads + (mb * NB + b) * 32 + lane] =
-                    make_float4(acc[mb][b][0], acc[mb][b][1], acc[mb][b][2], acc[mb][b][3]);
+        flush();
         __syncthreads();
         for (int i = tid; i < kQuads; i += kThreads) {
             float4 s = red[i];
