@@ -22,15 +22,16 @@ def _make(M, K, Ns, R, n, xt, wt, seed, mixed=True):
 def _check(x, A, B, y0, y, start, adapter, ranks, scaling):
     """Every row against the formula; rows without an adapter unchanged.
 
-    Bound, relative to S = |c| sum_r (sum_k |A x|) |B|: an fp32 x, and v, enter
-    as two tf32 pieces (2^-22 each); a tensor-core step of 8 products is taken
-    as 9 additions of 2^-23.  Eight warps share K at least: 2 x 4 steps for each
-    of a warp's at most ceil(K / 256) pieces of 32; up to 8 + 16 additions join
-    the warps and the parts of K, one product brings the scale; ranks take 4
-    steps per 16.  Then y: one addition (2^-24 of the result)."""
+    Bound, relative to S = |c| sum_r (sum_k |A x|) |B|: an fp32 x enters as two
+    tf32 pieces, v as pieces of B's type, each at most 2^-22 away; a tensor-core
+    step of k products is taken as k + 1 additions of 2^-23.  Eight warps share
+    K at least, so a warp has at most ceil(K / 256) pieces of 32, each of 8 steps
+    of 8 (or fewer additions: 2 of 16) and at most one addition to join it; up
+    to 8 + 8 additions join the warps and the parts of K, and the scale is one
+    product.  16 ranks take at most 3 steps of 16.  Then y: one addition (2^-24
+    of the result)."""
     n, R, K = A.shape
-    steps1, steps2 = 8 * math.ceil(K / 256), 4 * math.ceil(R / 16)
-    rel = 2 * 2.0 ** -22 + (9 * steps1 + 25 + 9 * steps2) * 2.0 ** -23
+    rel = 2 * 2.0 ** -22 + ((8 * 9 + 1) * math.ceil(K / 256) + 17 + 3 * 17 * math.ceil(R / 16)) * 2.0 ** -23
     seen = torch.zeros(x.shape[0], dtype=torch.bool)
     for i in range(len(adapter)):
         a, s0, s1 = int(adapter[i]), int(start[i]), int(start[i + 1])
