@@ -448,8 +448,9 @@ BC_API bc_status bc_lora_add(const void *x, bc_dtype x_dtype, const void *A, con
  * Masked tokens have the logit -inf (NaN counts as -inf, +inf as the largest
  * finite value); candidates of total -inf fill up the list where no others
  * are left.  beams <= 32, batch * beams <= 65535, V <= 2^22.
- * Totals are formed and compared in fp64; the sums of exponentials carry
- * fp32 exponentials (about 1e-7 relative).
+ * Totals are formed and compared in fp64; the sums of exponentials carry fp32
+ * exponentials.  A total is off by at most 7e-7 + 1.4e-7 a, a the mean distance of
+ * the row's logits to the largest one under its probabilities (at most log V).
  */
 BC_API bc_status bc_beam_select(const float *logits, const float *scores,
                                 const uint8_t *finished, int64_t batch, int64_t beams,

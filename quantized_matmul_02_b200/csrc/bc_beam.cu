@@ -13,17 +13,21 @@
 // second launch joins the spans of each beam and selects over a request's
 // beams.  HBM bound: 4 bytes per logit against about seven operations.
 //
-// Measured, on the GPU alone: 256 rows of 151936 logits, 16 candidates: 33 us,
-// 4.7 TB/s (lists of candidates above a running floor instead of the maxima:
-// 57 us, half of it their appending; rank counts: 163).  4 rows of 32003: 10 us.
+// Measured, on the GPU alone: 256 rows of 151936 logits, 16 candidates: 36 us,
+// 4.4 TB/s; with a fifth of the beams finished 34 us (lists of candidates above a
+// running floor instead of the maxima: 57 us, half of it their appending; rank
+// counts: 163).  4 rows of 32003: 10 us.
 //
 // Keys (value, place) are all distinct, so the result does not depend on the
 // order in which candidates are collected.
 //
-// Precision: exponentials in fp32 relative to a value near their maximum, eight
-// added in fp32, the rest in fp64, totals in fp64.  Order between beams is
-// decided on fp64 totals, so two candidates change places only where their
-// totals agree to about 1e-7.
+// Precision: exponentials in fp32, relative to the largest logit that a warp
+// has met, eight added in fp32; the rest and the totals in fp64.  The largest
+// one's term is exactly 1; one d below it is 2^-22 (the exponential's own error)
+// and 1.1 * 2^-23 d off (difference, product and log2(e) rounded).  So a total is
+// off by at most 2^-22 + 7 * 2^-24 + 1.1 * 2^-23 a, where a is the mean of d under the
+// row's probabilities, log V at most: 2e-6 if every rounding pointed one way.
+// Candidates of two beams change places only where their totals are as near.
 #include "bc_internal.cuh"
 
 #include <cooperative_groups.h>
@@ -73,7 +77,7 @@ constexpr float kLog2e = 1.44269504f;
 // (ord(logit), ~token).
 struct SpanOut {
     double sum;                                  // sum of exp(logit - max)
-    float max;                                   // or near it; -inf when nothing is above -inf
+    float max;                                   // -inf: nothing is above it
 };
 
 // The n largest of the block's keys, P per thread of W 32-bit words (most
@@ -191,8 +195,8 @@ __device__ __forceinline__ void scan_span(const SelectArgs &a, const int64_t r, 
     row -= skip;                                 // (never read before its first logit)
     const int tid = threadIdx.x, n_out = a.n_out;
     if (tid == 0) count = 0;
-    float m = -INFINITY;
-    double sum = 0;
+    float m = -INFINITY;                         // the warp's largest so far
+    double sum = 0;                              // of exp(logit - m)
     // element i of a thread's group in the tile that begins at t0
     auto place = [](int t0, int thread, int i) { return t0 + (i / 4 * kThreads + thread) * 4 + (i & 3); };
     auto load = [&](int t0, float (&x)[kPer]) {
@@ -233,18 +237,22 @@ __device__ __forceinline__ void scan_span(const SelectArgs &a, const int64_t r, 
 #pragma unroll
         for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
         uint32_t key = ord(top);
-        if (top > -INFINITY) {
-            // the reference follows a larger maximum only when it has to: sums of
-            // values up to exp(16) are as exact, and a change costs an fp64 exponential
-            if (top > m + 16.f || m == -INFINITY) {
-                sum *= exp((double)m - (double)top);
-                m = top;
-            }
+        // The warp's reference is the largest logit it has seen: that one's term is
+        // exactly 1, and the others' exponents are as near 0 as they can be.  A warp
+        // finds larger ones less and less often (1/t of its t-th tile), so the fp64
+        // exponential costs little.
+        if (__any_sync(0xffffffffu, top > m)) {
+            const float now = unord(__reduce_max_sync(0xffffffffu, key));
+            if (m > -INFINITY) sum *= exp((double)m - (double)now);
+            m = now;
+        }
+        if (m > -INFINITY) {
             float s[2] = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < kPer; ++i) s[i & 1] += exp2_fast((x[i] - m) * kLog2e);
             sum += (double)s[0] + (double)s[1];
-        } else if (!(t0 >= skip && t0 + kTile <= u1)) {
+        }
+        if (top == -INFINITY && !(t0 >= skip && t0 + kTile <= u1)) {
             bool any = false;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) any |= place(t0, tid, i) >= skip && place(t0, tid, i) < u1;

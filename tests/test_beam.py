@@ -223,6 +223,72 @@ def test_select_rejects_on_host():
         q.beam_select(torch.zeros(4, 9), torch.zeros(1, 4), 4)
 
 
+def _sum_bound(row):
+    """How far a row's log-sum-exp may be off.  With d a logit's distance to the
+    largest one and p its probability: the difference and its product with
+    log2(e) round by 2^-24 of themselves, the constant is 2^-26 off, so exp(-d)
+    is (2^-23 + 2^-26) d off, and 2^-22 by the exponential's own error; both are
+    weighted by p.  The largest one's term is exactly 1.  A thread's eight
+    terms take 7 roundings of 2^-24, the rest is in fp64."""
+    d = row.max() - row.astype(np.float64)
+    e = np.exp(-d)
+    p = e / e.sum()
+    return 2.0 ** -22 * (1 - p.max()) + (2.0 ** -23 + 2.0 ** -26) * (p * d).sum() + 7 * 2.0 ** -24
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,V", [(3, 102400), (640, 20480)])       # one launch, and two
+def test_near_certain_tokens(cuda_lib, batch, V):
+    """Rows with one token 8 to 15.9 above the next one, which the same thread
+    meets some tiles earlier, and all others 40 below: the sums are 1 and a
+    little.  That little is off by the second token's own error (2^-22 and 2^-23
+    + 2^-25 of its distance) and by the others, which may vanish beside 1."""
+    rng = np.random.default_rng(11)
+    logits = np.full((batch, V), -30.0, np.float32)
+    gap = rng.uniform(8, 15.9, batch)
+    first = rng.integers(0, 4096, batch)
+    later = first + 4096 * rng.integers(1, 4, batch)
+    top = rng.uniform(9.5, 10.5, batch).astype(np.float32)
+    logits[np.arange(batch), later] = top
+    logits[np.arange(batch), first] = top - gap
+    out, parent, token, _ = (t.cpu().numpy() for t in _select(cuda_lib, logits, np.zeros((batch, 1), np.float32), 2))
+    assert (token[:, 0] == later).all() and (token[:, 1] == first).all()
+    gap = top.astype(np.float64) - logits[np.arange(batch), first]
+    rest = (V - 2) * np.exp(-30.0 - top.astype(np.float64))
+    want = -np.log1p(np.exp(-gap) + rest)
+    bound = np.exp(-gap) * (2.0 ** -22 + gap * (2.0 ** -23 + 2.0 ** -25)) + 2 * rest
+    assert (np.abs(out[:, 0] - want) <= bound + 2.0 ** -24 * np.abs(want)).all(), np.abs(out[:, 0] - want).max()
+    assert (np.abs(out[:, 1] - (want - gap)) <= bound + 2.0 ** -24 * np.abs(want - gap)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,V", [(3, 102400), (640, 20480)])
+def test_sums_of_flat_and_spread_rows(cuda_lib, batch, V):
+    """Totals of rows whose weight lies far below the largest logit, or spreads."""
+    rng = np.random.default_rng(12)
+    logits = np.empty((batch, V), np.float32)
+    for b in range(batch):
+        kind = b % 4
+        if kind == 0:
+            logits[b] = -rng.uniform(2, 14)          # one value, each term off the same way
+            logits[b, rng.integers(0, V)] = rng.uniform(0, 1)
+        elif kind == 1:
+            logits[b] = rng.uniform(-20, 20, V)
+        elif kind == 2:
+            logits[b] = np.linspace(-12, rng.uniform(0, 12), V)         # every tile has a larger one
+        else:
+            logits[b] = 2.5 * rng.standard_normal(V)
+    row = logits.astype(np.float64)
+    top = row.max(1)
+    want = -np.log(np.exp(row - top[:, None]).sum(1))
+    scores = (-want).astype(np.float32)              # totals near 0, which rounding to fp32 leaves as they are
+    out, _, token, _ = (t.cpu().numpy()[:, 0] for t in _select(cuda_lib, logits, scores[:, None], 1))
+    assert (row[np.arange(batch), token] == top).all()
+    err = np.abs(out - (scores + want))
+    bound = np.array([_sum_bound(r) for r in logits])
+    assert (err <= bound + 2.0 ** -24 * np.abs(scores + want)).all(), [float((err / bound)[k::4].max()) for k in range(4)]
+
+
 # ---- reordering ----
 @pytest.mark.gpu
 @pytest.mark.parametrize("beams", [1, 2, 4, 5, 8, 13, 32])
