@@ -234,3 +234,37 @@ def test_norm_of_the_largest_values(cuda_lib, M, D):
     _near(cuda_lib.add_rmsnorm(x, None, EPS), v, _rel(D))
     if D % 64 == 0:
         _check_q8(cuda_lib.add_rmsnorm_q8(x, None, EPS), v, _rel(D))
+
+
+def _rows_that_stream(D):
+    """From here on a block stays and takes rows in turn: two rows for each of
+    the blocks of D / 8 threads (in warps) that 148 SMs hold, 1024 threads each."""
+    return 2 * 148 * (1024 // ((D // 8 + 31) // 32 * 32))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("xt,rt,wt,ot", [(F32, F32, F16, F32), (BF16, BF16, BF16, BF16), (F16, None, None, F32)])
+@pytest.mark.parametrize("D", [264, 320, 704, 1024, 1032, 2048, 4088])
+@pytest.mark.parametrize("more", [0, 1, 997])
+def test_norm_of_rows_in_turn(cuda_lib, D, more, xt, rt, wt, ot):
+    """Each width of block, with a full and a partly filled last warp."""
+    M = _rows_that_stream(D) + more
+    x, r, w = _inputs(M, D, xt, rt, wt, D)
+    h, v = _formula(x, r, w)
+    res = r if r is None else r.clone()
+    last = _step(ot) if ot != F32 else 0
+    _near(cuda_lib.add_rmsnorm(x, w, EPS, residual=res, out_dtype=ot), v, _rel(D) + last, 2.0 ** -25)
+    if r is not None:
+        _near(res, h, 2.0 ** -24 + _step(r.dtype), 2.0 ** -25)
+    if xt == ot:
+        cuda_lib.add_rmsnorm(x, w, EPS, residual=r, out=x)
+        _near(x, v, _rel(D) + last, 2.0 ** -25)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [320, 960, 1984, 4032])
+def test_norm_q8_of_rows_in_turn(cuda_lib, D):
+    x, r, w = _inputs(_rows_that_stream(D) + 3, D, F32, BF16, F16, D)
+    h, v = _formula(x, r, w)
+    _check_q8(cuda_lib.add_rmsnorm_q8(x, w, EPS, residual=r), v, _rel(D))
+    _near(r, h, 2.0 ** -24 + _step(BF16), 2.0 ** -25)
