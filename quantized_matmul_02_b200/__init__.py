@@ -483,7 +483,7 @@ def add_rmsnorm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float =
 
 class LoraDescs:
     """The projections of one lora_add_batched call (from make_lora_descs);
-    holds their tensors.  Keep it for the steps that use the same buffers."""
+    holds their tensors, whatever becomes of the list that it was made from.  Keep it for the steps that use the same buffers."""
     __slots__ = ("array", "count", "M", "R", "n_adapters", "x_dtype", "w_dtype", "device", "tensors")
 
 
@@ -525,7 +525,7 @@ def make_lora_descs(items: Sequence[tuple]) -> LoraDescs:
         fields += (xp, A.data_ptr(), B.data_ptr(), y.data_ptr(), N, K)
     d = LoraDescs()
     d.M, d.n_adapters, d.R, d.count, d.device = M, n, R, len(items), dev
-    d.x_dtype, d.w_dtype, d.tensors = _DT[xt], _DT[wt], items
+    d.x_dtype, d.w_dtype, d.tensors = _DT[xt], _DT[wt], tuple(map(tuple, items))
     d.array = struct.pack(f"{len(fields)}q", *fields)       # bc_lora_desc: six 8-byte fields
     return d
 
@@ -681,7 +681,8 @@ def matmul_q_beam(x: torch.Tensor, W: torch.Tensor, scales: Optional[torch.Tenso
 
 
 class BeamStates:
-    """States of beam_reorder (from make_beam_states); holds their tensors."""
+    """States of beam_reorder (from make_beam_states); holds their tensors,
+    whatever becomes of the list that it was made from."""
     __slots__ = ("array", "count", "beams_total", "device", "tensors")
 
 
@@ -721,7 +722,7 @@ def make_beam_states(tensors: Sequence[torch.Tensor]) -> BeamStates:
         beam = strides[0] if total > 1 else max(strides[0], run)
         fields += (t.data_ptr(), rows, run * size, row_stride * size, beam * size)
     st = BeamStates()
-    st.beams_total, st.device, st.tensors, st.count = total, dev, tensors, len(tensors)
+    st.beams_total, st.device, st.tensors, st.count = total, dev, tuple(tensors), len(tensors)
     st.array = struct.pack(f"{len(fields)}q", *fields)      # bc_beam_state: five 8-byte fields
     return st
 

@@ -1,6 +1,7 @@
 """Low-rank adapters of many requests (bc_lora_add, bc_lora_add_batched)
 against the formula in 64 bits, and the refusals."""
 import math
+import weakref
 
 import pytest
 import torch
@@ -191,3 +192,35 @@ def test_lora_wrapper_refuses(cuda_lib):
                 (x, A, B, y.cpu(), st, ad), (x, A.transpose(1, 2), B, y, st, ad)):
         with pytest.raises(ValueError):
             cuda_lib.lora_add(*bad)
+
+
+class _OnGpu:
+    """What the wrappers ask of a CUDA tensor, without one."""
+
+    def __init__(self, shape, dtype):
+        self._t = torch.empty(shape, dtype=dtype)
+        self.shape, self.dtype = self._t.shape, dtype
+        self.dim, self.stride, self.numel = self._t.dim, self._t.stride, self._t.numel
+        self.is_contiguous, self.data_ptr, self.element_size = self._t.is_contiguous, self._t.data_ptr, self._t.element_size
+
+    def get_device(self):
+        return 0
+
+
+def test_descriptors_hold_their_tensors():
+    """A list that is cleared or refilled after the call takes nothing away."""
+    import quantized_matmul_02_b200 as q
+    made = lambda: [_OnGpu((4, 64), F32), _OnGpu((2, 8, 64), F16), _OnGpu((2, 24, 8), F16), _OnGpu((4, 24), F32)]  # noqa: E731
+    items = [made(), made()]
+    alive = [weakref.ref(t) for i in items for t in i]
+    d = q.make_lora_descs(items)
+    items[0].clear()
+    items.clear()
+    assert all(r() is not None for r in alive) and d.count == 2
+    del d
+    assert all(r() is None for r in alive)
+    states = [_OnGpu((4, 8), F32), _OnGpu((4, 3, 8), BF16)]
+    alive = [weakref.ref(t) for t in states]
+    st = q.make_beam_states(states)
+    states.clear()
+    assert all(r() is not None for r in alive) and st.count == 2
