@@ -399,8 +399,8 @@ typedef struct bc_lora_desc {
  *                added.  Ranks behind ranks[a] are not used, whatever they hold.
  *   scaling      fp32 [n_adapters], device, or NULL (1)
  *   workspace    at least bc_workspace_size_lora() bytes, 256-byte aligned;
- *                its contents on entry do not matter; overlapping calls must
- *                not share it
+ *                its contents on entry do not matter; it may overlap nothing
+ *                else, and overlapping calls must not share it
  * fp32 arithmetic throughout; the order of the sums is fixed, so equal calls
  * give equal bits.
  */

@@ -939,7 +939,14 @@ bc_status bc_lora_add_batched(const bc_lora_desc *descs, int count, int64_t M, i
             overlap(d.y, yb, ranks, 4 * n_adapters) || overlap(d.y, yb, scaling, 4 * n_adapters) ||
             overlap(d.y, yb, workspace, need))
             return BC_ERR_INVALID_ARG;
+        if (overlap(workspace, need, d.x, (size_t)M * d.K * (x_dtype == BC_F32 ? 4 : 2)) ||
+            overlap(workspace, need, d.A, ab * d.K) || overlap(workspace, need, d.B, ab * d.N))
+            return BC_ERR_INVALID_ARG;
     }
+    if (overlap(workspace, need, seg_start, 4 * (n_segments + 1)) ||
+        overlap(workspace, need, seg_adapter, 4 * n_segments) || overlap(workspace, need, ranks, 4 * n_adapters) ||
+        overlap(workspace, need, scaling, 4 * n_adapters))
+        return BC_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < need) return BC_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return BC_ERR_ALIGNMENT;
     LoraArgs a;

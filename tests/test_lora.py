@@ -1,5 +1,6 @@
 """Low-rank adapters of many requests (bc_lora_add, bc_lora_add_batched)
 against the formula in 64 bits, and the refusals."""
+import ctypes
 import math
 import weakref
 
@@ -224,3 +225,18 @@ def test_descriptors_hold_their_tensors():
     st = q.make_beam_states(states)
     states.clear()
     assert all(r() is not None for r in alive) and st.count == 2
+
+
+@pytest.mark.parametrize("where", range(7))
+def test_lora_refuses_scratch_over_what_it_reads(where):
+    """x, A, B, the segments, the adapters, ranks and scaling: from their first
+    byte, and scratch that only reaches their first."""
+    import quantized_matmul_02_b200 as q
+    at = [FAKE + (i << 26) for i in range(10)]
+    M, N, K, R, n, S = 4, 32, 64, 8, 2, 4
+    d = q.LoraDesc(at[0], at[1], at[2], at[3], N, K)
+    need = q.lib.bc_workspace_size_lora(ctypes.byref(d), 1, M, R, n, S, 0)
+    target = (at[0], at[1], at[2], at[4], at[5], at[6], at[7])[where]
+    for ws in (target, target - (need - 1) // 256 * 256):
+        assert q.lib.bc_lora_add(at[0], 0, at[1], at[2], 1, M, N, K, R, n, at[4], at[5], S, at[6], at[7], at[3],
+                                 ws, need, None) == 1
