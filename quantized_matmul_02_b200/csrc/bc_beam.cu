@@ -816,9 +816,17 @@ bc_status bc_matmul_q_beam(const void *x, bc_dtype x_dtype, const void *W_or_pac
     const size_t rows = (size_t)M, no = (size_t)(batch * n_out);
     const void *out[] = {out_scores, parent, token, out_finished, workspace};
     const size_t out_len[] = {no * 4, no * 4, no * 4, no, need};
+    // what the matmul reads: packed codes with fp16 scales, or fp16 weights with fp32 scales or ranges
+    const bool packed = mode == BC_MODE_PACKED;
+    const bool scaled = packed || bits != 16;
+    const size_t groups = scaled ? (size_t)N * (group == 64 ? K / 64 : 1) * (packed ? 2 : 4) : 0;
+    const void *in[] = {x, W_or_packed, scales, zeros, beam_scores, finished};
+    const size_t in_len[] = {rows * K * (x_dtype == BC_F32 ? 4 : 2),
+                             packed ? (size_t)N * K * (bits > 0 ? bits : 0) / 8 : (size_t)N * K * 2, groups,
+                             mode == BC_MODE_RUNTIME_RANGE ? 0 : groups, rows * 4, rows};
     for (int i = 0; i < 5; ++i) {
-        if (overlap(out[i], out_len[i], beam_scores, rows * 4) || overlap(out[i], out_len[i], finished, rows))
-            return BC_ERR_INVALID_ARG;
+        for (int j = 0; j < 6; ++j)
+            if (in_len[j] && overlap(out[i], out_len[i], in[j], in_len[j])) return BC_ERR_INVALID_ARG;
         for (int j = 0; j < i; ++j)
             if (overlap(out[i], out_len[i], out[j], out_len[j])) return BC_ERR_INVALID_ARG;
     }

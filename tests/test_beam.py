@@ -289,6 +289,31 @@ def test_sums_of_flat_and_spread_rows(cuda_lib, batch, V):
     assert (err <= bound + 2.0 ** -24 * np.abs(scores + want)).all(), [float((err / bound)[k::4].max()) for k in range(4)]
 
 
+@pytest.mark.parametrize("mode,bits", [(0, 16), (0, 3), (1, 4), (2, 5)])       # runtime, packed, ranges
+def test_head_and_selection_refuse_outputs_over_what_the_matmul_reads(mode, bits):
+    """x, W, scales and zeros, from their first byte and to their last."""
+    import quantized_matmul_02_b200 as q
+    batch, beams, N, K, n_out = 2, 4, 1000, 128, 8
+    at = [FAKE + (i << 24) for i in range(12)]
+    need = q.workspace_size_matmul_beam(batch, beams, N, K, n_out, mode)
+    sizes = {0: batch * beams * K * 4, 1: N * K * bits // 8 if mode == 1 else N * K * 2}
+    if bits != 16:
+        sizes[2] = N * (K // 64) * (2 if mode == 1 else 4)
+        if mode != 2:
+            sizes[3] = sizes[2]
+
+    def call(**kw):
+        a = dict(x=at[0], xt=0, W=at[1], s=at[2] if 2 in sizes else None, z=at[3] if 3 in sizes else None, batch=batch,
+                 beams=beams, N=N, K=K, bits=bits, group=64, mode=mode, scores=at[4], finished=None, n_out=n_out, eos=-1,
+                 pad=0, out=at[5], parent=at[6], token=at[7], ended=at[8], ws=at[9], wsb=need, stream=None)
+        return q.lib.bc_matmul_q_beam(*{**a, **kw}.values())
+
+    for i, size in sizes.items():
+        for name in ("out", "parent", "token", "ended"):
+            assert call(**{name: at[i]}) == 1 and call(**{name: at[i] + size - 4}) == 1
+        assert call(ws=at[i]) == 1 and call(ws=at[i] + (size - 1) // 256 * 256) == 1
+
+
 # ---- reordering ----
 @pytest.mark.gpu
 @pytest.mark.parametrize("beams", [1, 2, 4, 5, 8, 13, 32])
