@@ -356,8 +356,11 @@ def matmul_q_argmax(x: torch.Tensor, W: torch.Tensor, scales: Optional[torch.Ten
 _F32, _F16, _BF16 = torch.float32, torch.float16, torch.bfloat16
 _I32, _U8 = torch.int32, torch.uint8
 _FLOATS = (_F32, _F16, _BF16)
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The calls behind torch.cuda.current_device and current_stream, without their
+# wrappers' cost; a torch that lacks them (one without CUDA does) has the latter.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _one_device(what: str, first: torch.Tensor, *tensors: Optional[torch.Tensor]) -> int:

@@ -3,6 +3,8 @@ rejects bad arguments on the host before touching the GPU (CPU only)."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 
@@ -97,3 +99,21 @@ def test_other_calls_reject_on_host(qmm):
                                 FAKE, 4096, None) == 1
     assert L.bc_matmul_q_argmax(FAKE, 0, FAKE, None, None, 1, 1 << 20, 64, 16, 64, 0, FAKE,
                                 FAKE, 4096, None) == 4
+
+
+def test_imports_under_a_torch_without_cuda():
+    """The host checks need no GPU, and no torch that was built for one."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import quantized_matmul_02_b200 as q
+assert q.lib.bc_add_rmsnorm(None, 0, None, 0, None, 0, 4, 64, 1e-6, None, 0, None) == 1
+try:
+    q.add_rmsnorm(torch.zeros(2, 8), None)
+except ValueError:
+    print("refused")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["refused"], r.stderr
