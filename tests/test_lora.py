@@ -240,3 +240,74 @@ def test_lora_refuses_scratch_over_what_it_reads(where):
     for ws in (target, target - (need - 1) // 256 * 256):
         assert q.lib.bc_lora_add(at[0], 0, at[1], at[2], 1, M, N, K, R, n, at[4], at[5], S, at[6], at[7], at[3],
                                  ws, need, None) == 1
+
+
+def _exact(x, A, B, start, adapter, ranks, scaling):
+    """c B (A x) of each row in 64 bits."""
+    out = torch.zeros((x.shape[0], B.shape[1]), dtype=torch.float64, device=x.device)
+    for i, a in enumerate(adapter):
+        keep = A.shape[1] if ranks is None else int(ranks[a])
+        s = slice(start[i], start[i + 1])
+        out[s] = float(scaling[a]) * (x[s].double() @ A[a, :keep].double().T) @ B[a, :, :keep].double().T
+    return out
+
+
+def _ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("xt", [F32, BF16])
+@pytest.mark.parametrize("wt", [F16, BF16])
+@pytest.mark.parametrize("start,K,N,R", [
+    (list(range(65)), 2176, 260, 32), (list(range(0, 65, 8)), 896, 130, 128), (list(range(41)), 4096, 130, 16),
+    ([0, 300, 777], 4864, 896, 128), ([0, 100, 400], 2176, 100, 24), ([0, 1000], 1024, 333, 64)])
+def test_every_piece_counts(cuda_lib, start, K, N, R, xt, wt):
+    """The root of the mean squared error over random signs, relative to that of
+    the result, where the worst case of every rounding at once says little.
+    Expected: an fp32 x in two tf32 pieces and v in pieces, at most 2^-22 of a
+    value off and below 2^-23 in this mean, each; sums in parts of 16 tensor-core
+    steps that lose up to an accumulator's last bit, 2^-23 of what they hold, on
+    average half of it, and no part larger than the whole: sqrt(16) * 2^-24 =
+    2^-22 if they were independent, for A x, and (3 * R / 16)^0.5 * 2^-24 for B v,
+    2^-21.7 at rank 128; roots of squares: 2^-21.  Losses of one part have one sign,
+    so twice that is allowed, 2^-20.  One piece less is far above: x in one tf32
+    piece 2^-13, v in two bf16 pieces 2^-18, v in one fp16 piece 2^-13."""
+    n, M = 5, start[-1]
+    x, mats, _, scaling = _make(M, K, (N,), R, n, xt, wt, K + N, mixed=False)
+    A, B, _ = mats[0]
+    adapter = [i % n for i in range(len(start) - 1)]
+    y = torch.zeros((M, N), device="cuda")
+    cuda_lib.lora_add(x, A, B, y, _ints(start), _ints(adapter), scaling=scaling)
+    want = _exact(x, A, B, start, adapter, None, scaling)
+    rel = float((y.double() - want).norm() / want.norm())
+    assert rel <= 2.0 ** -20, rel * 2 ** 24
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("xt,M", [(F32, 4900), (BF16, 9600)])
+@pytest.mark.parametrize("wt", [F16, BF16])
+@pytest.mark.parametrize("K", [4096, 12288])
+def test_long_sums_are_taken_in_parts(cuda_lib, K, M, xt, wt):
+    """Enough rows that K is not divided among blocks, and values of one sign, so
+    that what the tensor cores cut off adds up.  A step cuts off half of the
+    accumulator's last bit on average, up to 2^-24 of it: a part of 16 steps
+    loses 16 * 2^-24 / 2 = 2^-21 of itself, as its sum grows; v's three steps and
+    the other roundings are beside it.  In one sum K = 12288 takes 96 steps a warp
+    or more, which would lose 2^-18.4."""
+    R, N = 16, 24
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = (0.5 + torch.rand((M, K), generator=g, device="cuda")).to(xt)
+    A = ((0.5 + torch.rand((2, R, K), generator=g, device="cuda")) / K).to(wt)
+    B = (0.5 + torch.rand((2, N, R), generator=g, device="cuda")).to(wt)
+    y, scaling = torch.zeros((M, N), device="cuda"), torch.ones(2, device="cuda")
+    start, adapter = [0, M // 3, M], [1, 0]
+    cuda_lib.lora_add(x, A, B, y, _ints(start), _ints(adapter), scaling=scaling)
+    want = _exact(x, A, B, start, adapter, None, scaling)
+    lost = float(((want - y.double()) / want).mean())
+    assert abs(lost) <= 2.0 ** -20, lost * 2 ** 24
+    x2, mats, ranks, scaling = _make(M, K, (N,), R, 3, xt, wt, K, mixed=False)
+    A, B, y = mats[0][0], mats[0][1], torch.zeros((M, N), device="cuda")
+    cuda_lib.lora_add(x2, A, B, y, _ints(start), _ints(adapter), scaling=scaling)
+    want = _exact(x2, A, B, start, adapter, None, scaling)
+    assert float((y.double() - want).norm() / want.norm()) <= 2.0 ** -20
