@@ -314,6 +314,56 @@ def test_head_and_selection_refuse_outputs_over_what_the_matmul_reads(mode, bits
         assert call(ws=at[i]) == 1 and call(ws=at[i] + (size - 1) // 256 * 256) == 1
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,beams,V,n_out", [
+    (2, 32, 151936, 64),        # 9 spans a beam, 288 lists a request
+    (1, 32, 151936, 64),        # 18 spans, 576 lists
+    (16, 8, 100000, 16),        # 4 spans
+    (60, 3, 40003, 6),          # 3 spans, rows at odd places
+    (3, 16, 60001, 33)])
+def test_select_over_beams_of_several_spans(cuda_lib, batch, beams, V, n_out):
+    rng, logits, scores = _draw(batch, beams, V, V + beams)
+    scores = (0.1 * scores).astype(np.float32)          # many beams have a part in the result
+    fin = (rng.random((batch, beams)) < 0.2).astype(np.uint8)
+    _check(_select(cuda_lib, logits, scores, n_out), logits, scores, n_out)
+    _check(_select(cuda_lib, logits, scores, n_out, fin, eos=7, pad=11), logits, scores, n_out, fin, 7, 11)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,beams,V,n_out", [(1, 8, 40000, 16), (1, 8, 40000, 64), (700, 1, 60000, 8), (2, 32, 60000, 64),
+                                                 (1, 32, 151936, 64)])
+@pytest.mark.parametrize("values", [1, 3])
+def test_equal_totals_in_long_spans_and_many_lists(cuda_lib, batch, beams, V, n_out, values):
+    """More equal maxima than a list takes, in spans of more than eight tiles
+    and over many lists: beams share a row and a score, so the lowest places of
+    the first beam that has the best value win."""
+    row = np.random.default_rng(V).integers(0, values, V).astype(np.float32)
+    logits = np.broadcast_to(row, (batch * beams, V))
+    scores = np.full((batch, beams), -2.0, np.float32)
+    got = _select(cuda_lib, logits, scores, n_out)
+    at = np.nonzero(row == values - 1)[0][:n_out]
+    assert at.size == n_out
+    assert (got[1].cpu().numpy() == 0).all() and (got[2].cpu().numpy() == at).all()
+
+
+@pytest.mark.gpu
+def test_few_best_tokens_of_every_beam(cuda_lib):
+    """One token a beam stands out and the others are equal: what the beams'
+    first tokens leave is filled by the lowest places of the best beam."""
+    beams, V, n_out = 32, 100000, 64
+    logits = np.zeros((beams, V), np.float32)
+    top = 99999 - 3000 * np.arange(beams)
+    logits[np.arange(beams), top] = 5.0
+    scores = np.full((1, beams), -1.0, np.float32)
+    out, parent, token, _ = (t.cpu().numpy()[0] for t in _select(cuda_lib, logits, scores, n_out))
+    assert (np.sort(parent[:beams]) == np.arange(beams)).all() and (token[:beams] == top[parent[:beams]]).all()
+    # the beams' sums agree but for their last bits, so the rest is all of one beam
+    assert (parent[beams:] == parent[beams]).all() and (token[beams:] == np.arange(n_out - beams)).all()
+    near = _sum_bound(logits[0])
+    total = -1.0 - np.log(np.exp(logits[0].astype(np.float64)).sum())
+    assert (np.abs(out - np.where(np.arange(n_out) < beams, total + 5, total)) <= near + 2.0 ** -24 * 16).all()
+
+
 # ---- reordering ----
 @pytest.mark.gpu
 @pytest.mark.parametrize("beams", [1, 2, 4, 5, 8, 13, 32])
