@@ -161,14 +161,28 @@ int vec_of(const bc_beam_state &d) {
     return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
 }
 
-// Whether a state goes through shared memory: from 512 bytes a run, where its
-// pieces would have one or two bytes (448 MB of such runs: 226 us against 975;
-// with 4-byte pieces 140 against 107, with 8-byte ones 96 against 35).
-bool by_bytes(const bc_beam_state &d) { return d.row_bytes >= 512 && vec_of(d) < 4; }
+// Whether a state goes through shared memory: long runs whose pieces would have
+// one or two bytes.  Both ways, in us, pieces first; a block costs about as much
+// however short its run is, and pays sooner where it holds more beams:
+//   4 beams of 16 states, 8 requests, 8 runs of 256,000 bytes (1.5 GB read and
+//     written): pieces of 1 byte 1866 and 591, 2: 982 and 605, 4: 531 and 582,
+//     8: 316 and 544 (16-byte pieces: 238)
+//   runs of 1001, 2001, 4001 bytes, 1-byte pieces: 2 beams 93 and 159, 231 and 181,
+//     275 and 107; 4 beams 151 and 431, 182 and 268, 179 and 128; 8 beams 144 and 345,
+//     144 and 170, 145 and 91; 16 beams 354 and 189, 356 and 104, 353 and 105; of 513
+//     bytes: 16 beams 350 and 374, 32 beams 304 and 207
+//   2002, 4002, 8002 bytes, 2-byte pieces: 2 beams 121 and 178, 145 and 105, 140 and
+//     49; 4 beams 98 and 263, 96 and 126, 97 and 59; 8 beams 80 and 165, 79 and 88, 79
+//     and 91; 32 beams 160 and 111, 157 and 111
+bool by_bytes(const bc_beam_state &d, int64_t beams) {
+    const int vec = vec_of(d);
+    if (vec > 2 || (vec == 2 && beams > 4 && beams <= 8)) return false;
+    return d.row_bytes >= vec * (beams <= 2 ? 1600 : beams <= 4 ? 3000 : beams <= 8 ? 2400 : beams <= 16 ? 1000 : 500);
+}
 // Pieces (of the widest access, or a block's tile) of a run.
 uint64_t units_of(const bc_beam_state &d, int64_t beams) {
     const int64_t tile = kTileBytes / (beams <= 4 ? 4 : beams <= 8 ? 8 : beams <= 16 ? 16 : 32);
-    return by_bytes(d) ? (uint64_t)((d.row_bytes + tile - 1) / tile) : (uint64_t)d.row_bytes / vec_of(d);
+    return by_bytes(d, beams) ? (uint64_t)((d.row_bytes + tile - 1) / tile) : (uint64_t)d.row_bytes / vec_of(d);
 }
 
 }  // namespace
@@ -220,7 +234,7 @@ extern "C" bc_status bc_beam_reorder(const bc_beam_state *states, int count, con
             uint64_t most = 0;
             for (; i < count && n < kMaxStates; ++i) {
                 const bc_beam_state &d = states[i];
-                if (by_bytes(d) != (bytes == 1)) continue;
+                if (by_bytes(d, beams) != (bytes == 1)) continue;
                 const uint64_t units = units_of(d, beams);
                 a.st[n++] = State{static_cast<uint8_t *>(d.data), d.rows > 1 ? d.row_stride : 0, d.beam_stride,
                                   d.row_bytes, (uint32_t)d.rows, (uint32_t)units, vec_of(d)};
