@@ -661,12 +661,18 @@ __global__ void __launch_bounds__(kThreads) beam_cluster_kernel(const SelectArgs
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// One launch with a cluster per request while a block's share is at most ten
-// tiles and the clusters fit the GPU at once: 4 rows of 32003 take 10 us on the
-// GPU either way, and the host is busy for 17 us a call instead of 21.
+// One launch with a cluster per request while a block's span is at most ten
+// tiles and the clusters fit the GPU at once (two blocks per SM, but for places
+// that a cluster of eight cannot use).  The host is busy for 17 us a call instead
+// of 21.  On the GPU, one launch and two, in us (requests x beams x logits):
+//   1 x 4 x 32003 11.0 and 10.3, 1 x 1 x 151936 10.3 and 11.0, 1 x 8 x 40000 14.8 and
+//   19.5, 1 x 7 x 40000 14.3 and 13.7, 18 x 8 x 40000 17.5 and 18.6, 30 x 1 x 151936 12.3
+//   and 14.1, 32 x 4 x 32003 12.8 and 14.1, 28 x 5 x 32003 15.8 and 14.8;
+//   longer spans: 1 x 5 x 60000 15.8 and 13.0, 14 x 3 x 100000 15.4 and 14.2;
+//   more clusters: 37 x 4 x 32003 19.3 and 14.4, 55 x 8 x 40000 33.9 and 23.0
 bool clustered(int64_t batch, int64_t beams, int64_t V) {
     const int64_t tiles = (V + 3 + kTile - 1) / kTile;
-    return beams <= kCluster && beams * tiles <= 10 * kCluster && batch * kCluster <= 3 * kSms;
+    return beams <= kCluster && tiles <= kCluster / beams * 10 && batch <= 32;
 }
 // Spans per row: as many blocks as the GPU holds at once (four per SM: 256 rows
 // 34 us; half as many again 40, twice 42), none shorter than one tile; each
