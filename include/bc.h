@@ -338,7 +338,7 @@ BC_API size_t bc_workspace_size_argmax(int64_t M, int64_t N, int64_t K, bc_mode 
  *   out       [M][D] out_dtype, device, written; may be x itself when the
  *             types agree.  What is written may overlap nothing else.
  *   eps       above 0
- * Rows of a root mean square up to 1e18 (squares are summed in fp32).
+ * Values up to 1e18 (their squares are summed in fp32, scaled by the width).
  * Any M up to 2^24 and D up to 2^24.  Pointers need the alignment of their
  * element type; rows are read in 16-byte pieces when every pointer is 16-byte
  * aligned and D is a multiple of 8.

@@ -31,13 +31,11 @@ struct NormArgs {
     int D;
     float eps;
     int xt, rt, wt, ot;        // bc_dtype values; ot = kQ8 for codes
-    // Rows of more than kNarrow columns: squares are summed divided by 2^p, the
-    // power of two at or below D, so that a sum is at most twice the mean and
-    // large values stay in fp32.  (256 squares of 1e18 do as they are; per-head
-    // rows took 5.5 us with the products, 5.3 without.)
-    float unit, rest;          // 2^-p, and D / 2^p (both exact); 1 and D
+    // The sum of squares is divided by 2^p, the power of two at or below D, before
+    // threads join theirs: a row's is at most twice its mean then, and values up
+    // to 1e18 stay in fp32 at any width.
+    float unit, rest;          // 2^-p, and D / 2^p (both exact)
 };
-constexpr int kNarrow = 256;
 constexpr int kQ8 = 3;
 constexpr int64_t kSms = 148;
 constexpr int kResident = 1024;        // threads of norm_stream_kernel that an SM holds (60 registers each)
@@ -173,7 +171,6 @@ template <int TPR, int CH, bool VEC>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
 norm_kernel(const NormArgs a) {
     constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-    constexpr bool kScale = TPR * CH * 8 > kNarrow;
     __shared__ float sh[32];
     const int t = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
@@ -211,7 +208,7 @@ norm_kernel(const NormArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (!in) h[c][i] = 0.f;
-                ss = fmaf(kScale ? h[c][i] * a.unit : h[c][i], h[c][i], ss);
+                ss = fmaf(h[c][i], h[c][i], ss);
             }
         }
     } else {
@@ -235,10 +232,10 @@ norm_kernel(const NormArgs a) {
                     h[c][i] += unpack1(rr[c][i], a.rt);
                     if (live && col(c, i) < a.D) store1(a.res, base + col(c, i), a.rt, h[c][i]);
                 }
-                ss = fmaf(kScale ? h[c][i] * a.unit : h[c][i], h[c][i], ss);
+                ss = fmaf(h[c][i], h[c][i], ss);
             }
     }
-    ss = row_sum<TPR>(ss, sh);
+    ss = row_sum<TPR>(ss * a.unit, sh);
     const float rs = __frsqrt_rn(ss / a.rest + a.eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -304,7 +301,8 @@ __global__ void __launch_bounds__(MAXT, kResident / MAXT) norm_stream_kernel(con
         }
         float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(h[i] * a.unit, h[i], ss);
+        for (int i = 0; i < 8; ++i) ss = fmaf(h[i], h[i], ss);
+        ss *= a.unit;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
         if (lane == 0) sh[buf][warp] = ss;
@@ -430,7 +428,7 @@ bc_status run(NormArgs a, cudaStream_t s) {
     }
     const int D = a.D;
     int64_t power = 1;
-    while (D > kNarrow && 2 * power <= D) power *= 2;
+    while (2 * power <= D) power *= 2;
     a.unit = 1.f / (float)power;
     a.rest = (float)D * a.unit;
     // Two rows a block at least.  Measured with and without: 30000 x 1008 36.5
