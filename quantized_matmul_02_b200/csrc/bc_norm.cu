@@ -265,7 +265,7 @@ norm_kernel(const NormArgs a) {
     }
 }
 
-// Many rows of 257 to 4095 columns: a block stays and takes rows in turn, the
+// Many rows of 513 to 4095 columns: a block stays and takes rows in turn, the
 // next one's pieces on their way while this one's are summed and written; the
 // weights are read once.  Eight values a thread; blockDim is D / 8 rounded up
 // to warps.
@@ -431,10 +431,20 @@ bc_status run(NormArgs a, cudaStream_t s) {
     while (2 * power <= D) power *= 2;
     a.unit = 1.f / (float)power;
     a.rest = (float)D * a.unit;
-    // Two rows a block at least.  Measured with and without: 30000 x 1008 36.5
-    // and 44.5 us, 20000 x 1344 35 and 40; from 4096 columns on, where a block
-    // of the other kernel has two pieces a thread on their way, 52 and 50.5.
-    if (vec && D > 256 && D < 4096 && a.M >= 2 * kSms * (kResident / ((D / 8 + 31) / 32 * 32))) {
+    // A block that stays pays where it takes several rows and the other kernel's
+    // threads are badly filled (it holds 512, 1024, 2048 or 4096 columns), more so
+    // where a row has fewer bytes.  With and without, in us, bf16 / fp32 with a
+    // bf16 residual:
+    //   46875 x 640 39 and 47 / 50 and 58, 30000 x 1008 32.1 and 34.2 / 48.3 and 47.9,
+    //   23437 x 1280 33 and 41 / 47.5 and 52.6, 19531 x 1536 32.3 and 35.9 / 47.2 and 48.1,
+    //   13020 x 2304 32 and 46 / 49 and 57, 16741 x 1792 31.8 and 33.0 / 48.3 and 46.1,
+    //   8370 x 3584 31.5 and 34.6 / 48.6 and 47.0;
+    //   113636 x 264 59 and 52 / 73 and 67, 58593 x 512 31.6 and 30.5 / 48.1 and 45.5,
+    //   14648 x 2048 30.8 and 29.5 / 47.1 and 45.7, 8192 x 4096 33.9 and 35.4 / 52.5 and 50.8;
+    //   two rows a block: 2368 x 896 4.5 and 4.1 / 5.5 and 5.2
+    const int width = D <= 1024 ? 1024 : D <= 2048 ? 2048 : 4096;
+    if (vec && D > 512 && (D <= 1024 || 8 * D <= (a.res ? 6 : 7) * width) &&
+        a.M >= 4 * kSms * (kResident / ((D / 8 + 31) / 32 * 32))) {
         if (D <= 1024) launch_stream<128>(a, s);
         else if (D <= 2048) launch_stream<256>(a, s);
         else launch_stream<512>(a, s);

@@ -235,14 +235,14 @@ def test_norm_of_the_largest_values(cuda_lib, M, D):
 
 
 def _rows_that_stream(D):
-    """From here on a block stays and takes rows in turn: two rows for each of
+    """From here on a block stays and takes rows in turn: four rows for each of
     the blocks of D / 8 threads (in warps) that 148 SMs hold, 1024 threads each."""
-    return 2 * 148 * (1024 // ((D // 8 + 31) // 32 * 32))
+    return 4 * 148 * (1024 // ((D // 8 + 31) // 32 * 32))
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("xt,rt,wt,ot", [(F32, F32, F16, F32), (BF16, BF16, BF16, BF16), (F16, None, None, F32)])
-@pytest.mark.parametrize("D", [264, 320, 704, 1024, 1032, 2048, 4088])
+@pytest.mark.parametrize("D", [264, 320, 520, 704, 1024, 1032, 1536, 2048, 2056, 2560, 4088])
 @pytest.mark.parametrize("more", [0, 1, 997])
 def test_norm_of_rows_in_turn(cuda_lib, D, more, xt, rt, wt, ot):
     """Each width of block, with a full and a partly filled last warp."""
@@ -260,7 +260,7 @@ def test_norm_of_rows_in_turn(cuda_lib, D, more, xt, rt, wt, ot):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("D", [320, 960, 1984, 4032])
+@pytest.mark.parametrize("D", [320, 576, 960, 1088, 1984, 2112, 4032])
 def test_norm_q8_of_rows_in_turn(cuda_lib, D):
     x, r, w = _inputs(_rows_that_stream(D) + 3, D, F32, BF16, F16, D)
     h, v = _formula(x, r, w)
