@@ -354,8 +354,11 @@ BC_API bc_status bc_add_rmsnorm(const void *x, bc_dtype x_dtype, void *residual,
  * columns), which bc_matmul_q (BC_MODE_PACKED, bits = 8) reads as its W.
  *   v = the norm's output in fp32; lo = min(0, min v), hi = max(0, max v) of
  *   the 64 columns; scale = fp16((hi - lo) / 255), at least 2^-24 and at most
- *   65504; zero = round(-lo / scale); code = clamp(round(v / scale) + zero, 0, 255)
- * The range holds 0, so zero is a whole number in 0..255.  fp32 quotients.
+ *   65504; zero = min(round(-lo / scale), 255);
+ *   code = clamp(round(v / scale) + zero, 0, 255)
+ * The range holds 0, so zero is a whole number in 0..255.  round() is of the
+ * fp32 quotient here, half to even.  A row with a value that is not finite, which
+ * bc_add_rmsnorm passes on as NaN, has no form in codes: its codes mean nothing.
  *   D              a multiple of 64
  *   codes          uint8 [M][D], device, 8-byte aligned, written
  *   scales, zeros  fp16 [M][D/64], device, written
@@ -401,8 +404,12 @@ typedef struct bc_lora_desc {
  *   workspace    at least bc_workspace_size_lora() bytes, 256-byte aligned;
  *                its contents on entry do not matter; it may overlap nothing
  *                else, and overlapping calls must not share it
- * fp32 arithmetic throughout; the order of the sums is fixed, so equal calls
- * give equal bits.
+ * Sums are held in fp32.  Beside their roundings, an fp32 x is taken to 2^-22 of
+ * a value and v = scaling * A x to 2^-22, with fp16 adapters no finer than 2^-39
+ * of a row's largest v.  The order of the sums is fixed, so equal calls give
+ * equal bits; but it depends on how many rows share an adapter and on the sizes,
+ * so a row's last bits may change with the rest of the batch.  A value of x or
+ * v that is not finite makes its row of y NaN or infinite.
  */
 BC_API bc_status bc_lora_add_batched(const bc_lora_desc *descs, int count, int64_t M,
                                      int64_t R, int64_t n_adapters, bc_dtype x_dtype,

@@ -20,16 +20,20 @@
 // many rows, B's trips from L2 (once per 16 rows) and the tensor cores bind.
 //
 // Measured, on the GPU alone: 4100 rows of bf16, 4096 -> 2 x 12288, rank 16:
-// 135 us, 6.3 TB/s of the 847 MB that it must move (one fused kernel of
-// clusters that exchange v through distributed shared memory: 205 us; y read
-// and written in half sectors: 201 us).  64 rows over 48 adapters of rank 32,
-// 4096 -> 4096 + 2 x 1024: 18 us of 9.3.  One row, 896 -> 896 + 2 x 128: 9 us.
+// 163 us, 5.2 TB/s of the 847 MB that it must move.  The same with 2590 to 3860
+// of the rows in use, "4100 rows" below: 136 us of 105 (one fused kernel of clusters
+// that exchange v through distributed shared memory: 205 us; y read and written
+// in half sectors: 201 us).  64 rows over some 33 adapters of ranks 8, 15 and 32,
+// 4096 -> 4096 + 2 x 1024: 18 us of 3.9.  One row, 896 -> 896 + 2 x 128: 9 us.
 //
-// Precision: fp32 throughout.  Products of 16-bit values are exact in the
+// Precision: sums in fp32.  Products of 16-bit values are exact in the
 // tensor cores (of one type, or in tf32, which holds bf16 and fp16 exactly).
-// An fp32 x goes in as two tf32 pieces, 2^-22 of the value away; v as two or
-// three pieces of B's own type, as near, so that B needs no conversion.  Sums
-// run in a fixed order: results do not change from call to call.
+// An fp32 x goes in as two tf32 pieces, 2^-22 of the value away; v as pieces of
+// B's own type, so that B needs no conversion: three of bf16, 2^-25 away, or two of
+// fp16, 2^-22 away but no nearer than 2^-39 of the row's largest (a rank whose v
+// is below 2^-17 of that keeps fewer bits).  Sums run in a fixed order: results
+// do not change from call to call, but a row's depend on how many rows share its
+// adapter (kFew, tiles) and on the parts of K.
 #include "bc_internal.cuh"
 
 #include <mutex>
@@ -648,8 +652,8 @@ __device__ __forceinline__ void expand(const LoraArgs &a, const Desc &d, int di,
                       __float_as_uint(fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w)))));
     }
     // fp16 pieces are taken of v times 2^(141 - e), e the exponent bits of the
-    // row's largest: that one lies in 2^14 .. 2^15, and a piece's least step
-    // is 2^-40 of it.
+    // row's largest: that one lies in 2^14 .. 2^15, and a piece's least step,
+    // 2^-24, is at most 2^-38 of it.
     auto exponent = [&](int row) { return max((int)(top[row] >> 23), 15); };
     if (kHalf) __syncthreads();
 #pragma unroll
